@@ -99,6 +99,9 @@ _SIGS = {
                                            ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_fmt4_dequant": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                           ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_fmt4_linear_fwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                                             ctypes.c_void_p]),
     "qlora_launch_count": (ctypes.c_ulonglong, []),
     "qlora_profile_enable": (None, [ctypes.c_int]),
     "qlora_profile_read": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
@@ -150,6 +153,16 @@ def _hold(stream, *tensors):
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+
+
+_DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _same_device(what: str, *tensors):
+    """Every tensor of a call lives on one CUDA device."""
+    d = tensors[0].device
+    if d.type != "cuda" or any(t.device != d for t in tensors):
+        raise ValueError(f"{what}: all tensors must be on one CUDA device")
 
 
 @dataclass
@@ -351,6 +364,32 @@ def qlora_fmt4_dequant(codes: torch.Tensor, absmax: torch.Tensor, n: int, fmt: s
     _check(lib().qlora_fmt4_dequant(_ptr(codes), _ptr(absmax), n, FMT4[fmt], _ptr(out), _stream(stream)),
            "qlora_fmt4_dequant")
     return out
+
+
+def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, rows: int, fmt: str,
+                          Y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                          stream=None) -> torch.Tensor:
+    """Y [M, rows] = X W^T for a few tokens X (bf16 [M, cols]) and a [rows, cols] weight as
+    qlora_fmt4_quantize stores it (codes, absmax). Y is bf16 or fp32 (out_dtype, or Y's own dtype)."""
+    if X.dim() != 2 or X.dtype != torch.bfloat16:
+        raise ValueError("qlora_fmt4_linear_fwd: X must be a bf16 [M, cols] tensor")
+    M, cols = X.shape
+    if fmt not in FMT4:
+        raise ValueError(f"qlora_fmt4_linear_fwd: unknown format {fmt!r}")
+    if codes.dtype != torch.uint8 or absmax.dtype != torch.float32 or codes.numel() * 2 != rows * cols or \
+            absmax.numel() * 64 != rows * cols:
+        raise ValueError("qlora_fmt4_linear_fwd: codes (uint8) and absmax (fp32) must hold rows * cols weights")
+    if Y is None:
+        Y = torch.empty(M, rows, dtype=out_dtype, device=X.device)
+    if Y.shape != (M, rows) or Y.dtype not in _DTYPES or not Y.is_contiguous():
+        raise ValueError("qlora_fmt4_linear_fwd: Y must be a contiguous bf16 or fp32 [M, rows] tensor")
+    _same_device("qlora_fmt4_linear_fwd", X, codes, absmax, Y)
+    Xc, cc, ac = X.contiguous(), codes.contiguous(), absmax.contiguous()
+    with torch.cuda.device(X.device):
+        _check(lib().qlora_fmt4_linear_fwd(_ptr(Xc), M, _ptr(cc), _ptr(ac), rows, cols, FMT4[fmt], _ptr(Y),
+                                           _DTYPES[Y.dtype], _stream(stream)), "qlora_fmt4_linear_fwd")
+        _hold(stream, Xc, cc, ac)
+    return Y
 
 
 def qlora_linear_fwd(X: torch.Tensor, W: NF4Tensor, A: torch.Tensor | None, B: torch.Tensor | None, s: float,

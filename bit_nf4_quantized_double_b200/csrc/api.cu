@@ -305,6 +305,8 @@ qlora_status qlora_adamw_prefetch(const void *ptr, size_t bytes, int to_device, 
     return from_cuda(launch_prefetch(ptr, bytes, to_device != 0, static_cast<cudaStream_t>(stream)));
 }
 
+constexpr int64_t kFmt4LinearMaxM = 65535 * 16;      // sixteen tokens per row of the launch grid
+
 static bool fmt4_ok(qlora_fmt4 f) {
     return f == QLORA_FMT4_INT4 || f == QLORA_FMT4_FP4_E2M1 || f == QLORA_FMT4_FP4_E3M0;
 }
@@ -325,6 +327,17 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
         return QLORA_ERR_INVALID_ARG;
     return from_cuda(launch_fmt4_dequant(codes, absmax, n, fmt, static_cast<__nv_bfloat16 *>(W_out),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
+                                   int64_t cols, qlora_fmt4 fmt, void *Y, qlora_dtype ydt, qlora_stream_t stream) {
+    if (!X || !codes || !absmax || !Y || !aligned16(X) || !aligned16(codes) || !aligned16(Y) ||
+        (reinterpret_cast<uintptr_t>(absmax) & 3u) || !fmt4_ok(fmt) || (ydt != QLORA_F32 && ydt != QLORA_BF16))
+        return QLORA_ERR_INVALID_ARG;
+    if (M < 1 || rows < 1 || cols < 1 || cols % 64 != 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (M > kFmt4LinearMaxM || rows > (1LL << 31) || cols > (1LL << 30)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    return from_cuda(launch_fmt4_linear(static_cast<const __nv_bfloat16 *>(X), M, codes, absmax, rows, cols, fmt, Y,
+                                        ydt == QLORA_F32, static_cast<cudaStream_t>(stream)));
 }
 
 qlora_status qlora_get_device_status(qlora_stream_t stream) {

@@ -24,6 +24,8 @@ cudaError_t launch_fmt4_quantize(const void *W, qlora_dtype dt, int64_t n, qlora
                                  float *absmax, cudaStream_t st);
 cudaError_t launch_fmt4_dequant(const uint8_t *codes, const float *absmax, int64_t n, qlora_fmt4 f,
                                 __nv_bfloat16 *out, cudaStream_t st);
+cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
+                               int64_t cols, qlora_fmt4 f, void *Y, bool y_f32, cudaStream_t st);
 cudaError_t launch_adamw(float *theta, const float *g, float *m, float *v, int64_t n, float lr, float b1, float b2,
                          float eps, float wd, int64_t step, __nv_bfloat16 *out_bf16, cudaStream_t st);
 cudaError_t launch_prefetch(const void *ptr, size_t bytes, bool to_device, cudaStream_t st);

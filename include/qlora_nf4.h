@@ -382,6 +382,27 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
                                 void *W_out, qlora_stream_t stream);
 
 /*
+ * Product of a few tokens with a weight in one of these formats, straight from its codes
+ * (the page compares the formats by model quality; it has no counterpart of this call):
+ *   Y[m, n] = (1 / S) sum_b absmax[n, b] sum_{k in block b} v(code[n, k]) X[m, k],
+ * the weight's dequantisation before its rounding to bf16 (qlora_fmt4_dequant rounds each
+ * weight; here products are exact, sums fp32, and Y is rounded once).
+ *   X       bf16 [M, cols], 16-byte aligned; M >= 1 (made for M <= 16; more tokens read the
+ *           codes again for every 16), M <= 1048560;
+ *   codes   the codes of a [rows, cols] weight as qlora_fmt4_quantize stores its
+ *           rows * cols values, 16-byte aligned; cols % 64 == 0, any rows;
+ *   absmax  fp32 [rows, cols / 64], 4-byte aligned;
+ *   Y       [M, rows], bf16 or fp32 by ydt, 16-byte aligned.
+ * Every output is a sum in a fixed order. A NaN or infinity in X or absmax reaches the
+ * outputs whose sums hold it, as in the formula. One kernel launch; no workspace.
+ * QLORA_ERR_INVALID_ARG for a null or misaligned pointer, an unknown format or dtype;
+ * QLORA_ERR_UNSUPPORTED_SHAPE for sizes outside the rules above (or rows above 2^31, cols
+ * above 2^30).
+ */
+qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
+                                   int64_t cols, qlora_fmt4 fmt, void *Y, qlora_dtype ydt, qlora_stream_t stream);
+
+/*
  * Measurement hooks. The page has no counterpart: they let a benchmark count
  * and time the library's own kernels without a profiler.
  *   qlora_launch_count    kernel launches issued by this process so far.
