@@ -143,6 +143,21 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(what: str, fn, device: torch.device, stream, *args):
+    """fn(*args, stream) with `device` current and its status checked. A call made on the current
+    device's current stream, as most are, skips the device switch and the stream object."""
+    if stream is None and _raw_stream is not None and torch.cuda.current_device() == device.index:
+        status = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    if status != QLORA_OK:
+        raise QloraError(status, what)
+
+
 def _hold(stream, *tensors):
     """Temporaries made for a call (contiguous copies, a workspace) are freed when the
     wrapper returns, while the kernels queued on `stream` may still read them. torch's
@@ -158,10 +173,9 @@ def _hold(stream, *tensors):
 _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
 
 
-def _same_device(what: str, *tensors):
+def _same_device(what: str, device: torch.device, *tensors):
     """Every tensor of a call lives on one CUDA device."""
-    d = tensors[0].device
-    if d.type != "cuda" or any(t.device != d for t in tensors):
+    if device.type != "cuda" or any(t.device != device for t in tensors):
         raise ValueError(f"{what}: all tensors must be on one CUDA device")
 
 
@@ -374,21 +388,23 @@ def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Te
     if X.dim() != 2 or X.dtype != torch.bfloat16:
         raise ValueError("qlora_fmt4_linear_fwd: X must be a bf16 [M, cols] tensor")
     M, cols = X.shape
-    if fmt not in FMT4:
+    f = FMT4.get(fmt)
+    if f is None:
         raise ValueError(f"qlora_fmt4_linear_fwd: unknown format {fmt!r}")
     if codes.dtype != torch.uint8 or absmax.dtype != torch.float32 or codes.numel() * 2 != rows * cols or \
             absmax.numel() * 64 != rows * cols:
         raise ValueError("qlora_fmt4_linear_fwd: codes (uint8) and absmax (fp32) must hold rows * cols weights")
+    dev = X.device
     if Y is None:
-        Y = torch.empty(M, rows, dtype=out_dtype, device=X.device)
-    if Y.shape != (M, rows) or Y.dtype not in _DTYPES or not Y.is_contiguous():
+        Y = torch.empty(M, rows, dtype=out_dtype, device=dev)
+    ydt = _DTYPES.get(Y.dtype)
+    if ydt is None or Y.shape != (M, rows) or not Y.is_contiguous():
         raise ValueError("qlora_fmt4_linear_fwd: Y must be a contiguous bf16 or fp32 [M, rows] tensor")
-    _same_device("qlora_fmt4_linear_fwd", X, codes, absmax, Y)
+    _same_device("qlora_fmt4_linear_fwd", dev, codes, absmax, Y)
     Xc, cc, ac = X.contiguous(), codes.contiguous(), absmax.contiguous()
-    with torch.cuda.device(X.device):
-        _check(lib().qlora_fmt4_linear_fwd(_ptr(Xc), M, _ptr(cc), _ptr(ac), rows, cols, FMT4[fmt], _ptr(Y),
-                                           _DTYPES[Y.dtype], _stream(stream)), "qlora_fmt4_linear_fwd")
-        _hold(stream, Xc, cc, ac)
+    _launch("qlora_fmt4_linear_fwd", lib().qlora_fmt4_linear_fwd, dev, stream, Xc.data_ptr(), M, cc.data_ptr(),
+            ac.data_ptr(), rows, cols, f, Y.data_ptr(), ydt)
+    _hold(stream, Xc, cc, ac)
     return Y
 
 

@@ -397,7 +397,7 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
  * outputs whose sums hold it, as in the formula. One kernel launch; no workspace.
  * QLORA_ERR_INVALID_ARG for a null or misaligned pointer, an unknown format or dtype;
  * QLORA_ERR_UNSUPPORTED_SHAPE for sizes outside the rules above (or rows above 2^31, cols
- * above 2^30).
+ * above 2^27).
  */
 qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
                                    int64_t cols, qlora_fmt4 fmt, void *Y, qlora_dtype ydt, qlora_stream_t stream);
