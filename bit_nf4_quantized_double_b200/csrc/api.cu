@@ -335,7 +335,7 @@ qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *code
         (reinterpret_cast<uintptr_t>(absmax) & 3u) || !fmt4_ok(fmt) || (ydt != QLORA_F32 && ydt != QLORA_BF16))
         return QLORA_ERR_INVALID_ARG;
     if (M < 1 || rows < 1 || cols < 1 || cols % 64 != 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
-    if (M > kFmt4LinearMaxM || rows > (1LL << 31) || cols > (1LL << 27)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (M > kFmt4LinearMaxM || rows > (1LL << 30) || cols > (1LL << 27)) return QLORA_ERR_UNSUPPORTED_SHAPE;
     return from_cuda(launch_fmt4_linear(static_cast<const __nv_bfloat16 *>(X), M, codes, absmax, rows, cols, fmt, Y,
                                         ydt == QLORA_F32, static_cast<cudaStream_t>(stream)));
 }

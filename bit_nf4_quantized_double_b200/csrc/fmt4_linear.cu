@@ -27,15 +27,18 @@
 // instructions to place the codes, but on this part it runs as two fp16 mma with conversions
 // before them: 48 us where a [28672, 8192] weight's bytes take 20.)
 //
-// Layout. A warp keeps the token operands of one slice of 256 inputs in registers and runs
-// down the rows in steps of 16, which it copies into its own ring of stages (stream4.cuh).
-// The 16 warps of a CTA hold 16 slices, a cluster of CTAs the whole row; a tile of 16 rows is
-// summed over the warps, then over the CTAs, in a fixed order.
+// Layout. A warp keeps the token operands of one slice of 256 inputs in registers, converted
+// once, and runs down the rows in steps of 16 through its own ring of stages, which its lane 0
+// fills by TMA. The 16 warps of a CTA hold 16 slices, a cluster of CTAs the whole row; tiles of
+// 16 rows are summed over the warps every second step, over the CTAs at the end, in a fixed
+// order. (Tokens in shared memory and a whole row per warp need no sums, but a warp per tile is
+// 12 warps per SM at [28672, 8192], too few to hide the latencies of the products.)
 #include <algorithm>
 #include <atomic>
 
 #include "launch.h"
-#include "stream4.cuh"
+#include "tc.cuh"
+#include "tmap.h"
 
 namespace qnf4 {
 
@@ -46,65 +49,54 @@ namespace {
 constexpr int kF4Warps = 16;
 constexpr int kF4Threads = 32 * kF4Warps;
 constexpr int kF4Stages = 4;
-constexpr int kF4StageBytes = s4::kCodeBytes + s4::kStepRows * 16;   // codes, four fp32 constants per row
+constexpr int kF4StepK = 256;                                          // a step: 16 rows x 256 inputs,
+constexpr int kF4StepRows = 16;                                        // 128 bytes of codes per row
+constexpr int kF4StageBytes = kF4StepRows * 128;
+constexpr int kF4ScaleBytes = kF4StepRows * 16;                        // four block constants per row
 constexpr int kF4Tokens = 16;                                          // tokens per pass over the codes
 constexpr int kF4MaxCluster = 8;
-constexpr int kF4SegBytes = 16384;                                     // tile sums kept for the cluster's sum
+constexpr int kF4Round = 2;                                            // steps between sums over the warps
+static_assert(kF4Stages == 2 * kF4Round, "a round's stages are refilled while the other two are used");
 
-// Shared memory: 256 rows of 256 bytes whose first halves hold the lookup table (a word per
-// lane) and whose second halves ("holes", 32 floats each) the warps' sums; the rings; a barrier;
-// the tile sums of a cluster's segment.
-constexpr int kF4TableBytes = 65536;
-constexpr int kF4RingBytes = kF4Warps * kF4Stages * kF4StageBytes;
-constexpr int kF4BarBytes = 32;
-constexpr int f4_smem(bool cluster) { return kF4TableBytes + kF4RingBytes + kF4BarBytes + (cluster ? kF4SegBytes : 0); }
-static_assert(f4_smem(true) <= 232448, "shared memory");
+// Shared memory: the warps' rings of codes and of constants, two buffers of the warps' sums of a
+// round, the rings' barriers, the round's barrier and the abort flag, a cluster's tile sums.
+constexpr int kF4ScaleAt = kF4Warps * kF4Stages * kF4StageBytes;
+constexpr int kF4SumAt = kF4ScaleAt + kF4Warps * kF4Stages * kF4ScaleBytes;
+__host__ __device__ constexpr int f4_piece(int nt) { return 16 * 8 * nt * 4; }          // a warp's sums of a tile
+__host__ __device__ constexpr int f4_buf_bytes(int nt) { return kF4Round * kF4Warps * f4_piece(nt); }
+__host__ __device__ constexpr int f4_bar_at(int nt) { return kF4SumAt + 2 * f4_buf_bytes(nt); }
+__host__ __device__ constexpr int f4_seg_at(int nt) { return f4_bar_at(nt) + kF4Warps * kF4Stages * 8 + 32; }
+__host__ __device__ constexpr int f4_seg_tiles(int nt) { return 32 / nt; }
+constexpr int f4_smem(int nt, bool cluster) { return 1024 + f4_seg_at(nt) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0); }
+static_assert(f4_smem(1, true) <= 232448 && f4_smem(2, true) <= 232448, "shared memory");
 
-// A round is f4_round(nt) steps of every warp. Its sums go to one of two buffers and are added
-// over the warps after the first step of the next round, when the others have mostly written
-// theirs. A warp's sums of a tile are a piece of 128 nt floats, [token][row], permuted so that
-// the 32 lanes of a store (eight rows of four tokens 2 t, or of four tokens 2 t + 1) touch
-// every bank once.
-__host__ __device__ constexpr int f4_round(int nt) { return nt == 1 ? 2 : 1; }
-__host__ __device__ constexpr int f4_seg_tiles(int nt) { return kF4SegBytes / (128 * nt * 4); }
-__device__ __forceinline__ int f4_sum_at(int m, int r) { return ((m ^ ((m >> 2) & 1)) << 4) + (r ^ ((m & 2) << 2)); }
-// Byte offset of float x of piece p (both buffers' pieces count up to 64 / nt).
-template <int NT>
-__device__ __forceinline__ uint32_t f4_hole(int p, int x) {
-    return (uint32_t)(p * NT * 4 + (x >> 5)) * 256u + 128u + (uint32_t)(x & 31) * 4u;
+// A warp's sums of a tile are [token][row], permuted so that the 32 lanes of a store (eight even
+// or odd rows of tokens 2 t, or of tokens 2 t + 1) touch every bank once.
+__device__ __forceinline__ int f4_sum_at(int m, int r) {
+    return ((m ^ ((m >> 2) & 1)) << 4) + ((r >> 1) | (((r & 1) << 3) ^ ((m & 2) << 2)));
 }
 
 struct F4Args {
+    CUtensorMap codes;         // bytes [rows, K / 2], box of a step, 128-byte swizzle
+    CUtensorMap scales;        // fp32 [rows, K / 64], box of a step (vec_scales)
     const __nv_bfloat16 *X;
-    const uint8_t *codes;
     const float *absmax;
     void *Y;
     int64_t M, N;
     int K, kbs, nsl;           // inputs, 64-blocks and 256-input slices per row
     int wk;                    // warps along a row in a CTA; the CTA's 16 / wk tiles lie side by side
-    int nch, passes;           // CTAs along a row (cluster size); passes over the rows per segment
+    int nch, passes;           // CTAs along a row (cluster size); passes over a segment's rows
     int y_f32, vec_scales;
     uint32_t two2, two4, two8, two12;   // 2^2, 2^4, 2^8, 2^12
     float factor;              // (power of two of the decoded weights) / S
 };
 
 // Codes of a word as four fp16 pairs; pair_code names the codes of pair p (low half, high half).
-// Words 1 of Int4 and E3M0 come from the table, pair by byte: (0,1) (2,3) (4,5) (6,7).
 template <int FMT>
-__host__ __device__ constexpr bool from_table(int word) { return FMT != QLORA_FMT4_FP4_E2M1 && word == 1; }
-template <int FMT>
-__host__ __device__ constexpr int pair_code(int word, int p, int half) {
-    return from_table<FMT>(word)          ? 2 * p + half
-           : FMT == QLORA_FMT4_INT4       ? (p < 2 ? 1 - p : 5 - p) + 4 * half     // (1,5) (0,4) (3,7) (2,6)
-           : FMT == QLORA_FMT4_FP4_E2M1   ? 2 * p + 1 - half                        // (1,0) (3,2) (5,4) (7,6)
-                                          : (p < 2 ? 1 + 4 * p : 4 * (p - 2)) + 2 * half;   // (1,3) (5,7) (0,2) (4,6)
-}
-// A code's fp16 operand, for the table.
-template <int FMT>
-__device__ __forceinline__ uint32_t code_f16(uint32_t n) {
-    const uint32_t m = n & 7u, sign = (n & 8u) << 12;
-    if (FMT == QLORA_FMT4_INT4) return (m << 8) | sign;
-    return (m ? (m + 12u) << 10 : 0u) | sign;
+__host__ __device__ constexpr int pair_code(int p, int half) {
+    return FMT == QLORA_FMT4_INT4       ? (p < 2 ? 1 - p : 5 - p) + 4 * half     // (1,5) (0,4) (3,7) (2,6)
+           : FMT == QLORA_FMT4_FP4_E2M1 ? 2 * p + 1 - half                        // (1,0) (3,2) (5,4) (7,6)
+                                        : (p < 2 ? 1 + 4 * p : 4 * (p - 2)) + 2 * half;   // (1,3) (5,7) (0,2) (4,6)
 }
 __device__ __forceinline__ uint32_t f16x2_of_e3m2(uint16_t v) {
     uint32_t d;
@@ -112,14 +104,8 @@ __device__ __forceinline__ uint32_t f16x2_of_e3m2(uint16_t v) {
     return d;
 }
 template <int FMT>
-__device__ __forceinline__ void decode(const F4Args &a, const uint8_t *table, uint32_t lane4, int word, uint32_t w,
-                                       uint32_t (&p)[4]) {
-    if (from_table<FMT>(word)) {
-        // address = byte * 256 + lane * 4, by one permute
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p[i] = *reinterpret_cast<const uint32_t *>(table + prmt(w, lane4, 0x5504u | ((uint32_t)i << 4)));
-    } else if (FMT == QLORA_FMT4_INT4) {
+__device__ __forceinline__ void decode(const F4Args &a, uint32_t w, uint32_t (&p)[4]) {
+    if (FMT == QLORA_FMT4_INT4) {
         const uint32_t w4 = w * a.two4, w8 = w * a.two8, w12 = w * a.two12;
         p[0] = (w8 & 0x07000700u) | (w12 & 0x80008000u);
         p[1] = (w4 & 0x07000700u) | (w8 & 0x80008000u);
@@ -159,7 +145,7 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
 // Token operands of one slice (256 inputs from k0) for up to eight tokens from X: lane (g, t)
 // holds token g, inputs 64 b + 16 t + 8 j + 0..7 in xb[8 b + 4 j + p], in the order of the
 // decoded pairs. Lane u converts inputs 8 u .. 8 u + 7 of every token, which are one such
-// group, and hands them over in shared memory (stage(m, u)).
+// group, and hands them over in shared memory (stage(m, u): 512 bytes for each of four tokens).
 // up0, up1: 2^e of the tokens of accumulator columns 2 t and 2 t + 1.
 template <int FMT, typename Stage>
 __device__ __forceinline__ void f4_tokens(const __nv_bfloat16 *X, int mn, int K, int k0, int lane, Stage stage,
@@ -174,8 +160,14 @@ __device__ __forceinline__ void f4_tokens(const __nv_bfloat16 *X, int mn, int K,
     }
     up0 = up1 = 0.0f;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        if (m < mn) {
+    for (int i = 0; i < 32; ++i) xb[i] = 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (4 * h >= mn) break;
+#pragma unroll
+        for (int mm = 0; mm < 4; ++mm) {
+            const int m = 4 * h + mm;
+            if (m >= mn) break;
             const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
             // |x| of the largest, as bf16 bits
             uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
@@ -190,71 +182,65 @@ __device__ __forceinline__ void f4_tokens(const __nv_bfloat16 *X, int mn, int K,
                 f[2 * i] = bf16_lo(w[i]) * down;
                 f[2 * i + 1] = bf16_hi(w[i]) * down;
             }
-            uint32_t o[4];                                 // this lane's inputs are word lane % 2 of a block
+            uint32_t o[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                constexpr bool same = !from_table<FMT>(1);
-                const float l0 = f[pair_code<FMT>(0, p, 0)], h0 = f[pair_code<FMT>(0, p, 1)];
-                const float l1 = f[pair_code<FMT>(1, p, 0)], h1 = f[pair_code<FMT>(1, p, 1)];
-                o[p] = same ? f16x2_of(l0, h0) : f16x2_of((lane & 1) ? l1 : l0, (lane & 1) ? h1 : h0);
-            }
-            *stage(m & 3, lane) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int p = 0; p < 4; ++p) o[p] = f16x2_of(f[pair_code<FMT>(p, 0)], f[pair_code<FMT>(p, 1)]);
+            *stage(mm, lane) = make_uint4(o[0], o[1], o[2], o[3]);
             up0 = 2 * t == m ? up : up0;
             up1 = 2 * t + 1 == m ? up : up1;
         }
-        if ((m & 3) == 3) {                            // four tokens are staged: their lanes take them
-            __syncwarp();
+        __syncwarp();
+        if ((g >> 2) == h && g < mn) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                if (g < mn) o = *stage(g & 3, 8 * (i >> 1) + 2 * t + (i & 1));
-                if ((g >> 2) == (m >> 2)) {
-                    xb[4 * i] = o.x;
-                    xb[4 * i + 1] = o.y;
-                    xb[4 * i + 2] = o.z;
-                    xb[4 * i + 3] = o.w;
-                }
+                const uint4 o = *stage(g & 3, 8 * (i >> 1) + 2 * t + (i & 1));
+                xb[4 * i] = o.x;
+                xb[4 * i + 1] = o.y;
+                xb[4 * i + 2] = o.z;
+                xb[4 * i + 3] = o.w;
             }
-            __syncwarp();
         }
+        __syncwarp();                                  // before the next tokens' hand-over
     }
 }
 
-// Copies of one step: 16 rows from `codes` and `absmax` (the tile's first row, this lane's
-// offsets added), of which `rows` are the weight's; a lane past the last input copies zeros.
-struct F4Lane {
-    uint32_t dst, code_off, scale_off;   // stage offset of the lane's first chunk; global byte offsets
-    int row0;                            // first row of the warp's tile in the CTA's group
-    int bytes;                           // 16, or 0 for a chunk past the end of the row
-};
-__device__ __forceinline__ void f4_issue(const F4Args &a, uint32_t stage, const uint8_t *codes, const float *absmax,
-                                         int rows, const F4Lane &l, int s, int lane) {
-    const uint32_t rb = (uint32_t)a.K / 2;
-    const uint8_t *scales = reinterpret_cast<const uint8_t *>(absmax);
-    const uint32_t dst = stage + l.dst;                // rows r + 4 i swizzle alike
-    const uint32_t sc = stage + s4::kCodeBytes;
-    if (rows >= s4::kStepRows && a.vec_scales) {
+// Asynchronous copy of 4 bytes, or of none: zeros.
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Block constants of one step where a row's do not start on 16 bytes: rows row0 .., blocks 4 s ..
+// (zeros past the last row and block), block lane % 4 of rows lane / 4 and + 8.
+__device__ __forceinline__ void f4_scales(const F4Args &a, uint32_t dst, int64_t row0, int s, int lane) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s4::cp16n(dst + 512 * i, codes + (l.code_off + 4 * i * rb), l.bytes);
-        if (lane < 16) s4::cp16n(sc + lane * 16, scales + l.scale_off, 16);
-        return;
+    for (int i = 0; i < 2; ++i) {
+        const int q = 8 * i + (lane >> 2), b = 4 * s + (lane & 3);
+        const bool ok = row0 + q < a.N && b < a.kbs;
+        cp4(dst + q * 16 + (lane & 3) * 4, ok ? a.absmax + (row0 + q) * a.kbs + b : a.absmax, ok);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool ok = (lane >> 3) + 4 * i < rows;
-        s4::cp16n(dst + 512 * i, ok ? codes + (l.code_off + 4 * i * rb) : a.codes, ok ? l.bytes : 0);
-    }
-    if (a.vec_scales) {
-        const bool ok = lane < rows;
-        if (lane < 16) s4::cp16n(sc + lane * 16, ok ? scales + l.scale_off : (const uint8_t *)a.absmax, ok ? 16 : 0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int q = 8 * i + (lane >> 2), b = 4 * s + (lane & 3);
-            const bool ok = q < rows && b < a.kbs;
-            s4::cp4n(sc + q * 16 + (lane & 3) * 4, ok ? absmax + (int64_t)(l.row0 + q) * a.kbs + b : a.absmax, ok ? 4 : 0);
-        }
-    }
+}
+
+// A bounded wait whose loop is out of line.
+__device__ __noinline__ bool f4_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool f4_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return mbar_try_wait(bar, parity) || f4_wait_slow(bar, parity, abort);
+}
+
+// Before an early exit: waits, within a limit, for the copies of the stages in `flying`.
+__device__ __noinline__ void f4_drain(uint32_t full, uint32_t flying, uint32_t parity) {
+    cp_wait<0>();
+    const uint64_t t0 = global_timer_ns();
+    for (int s = 0; s < kF4Stages; ++s)
+        while (((flying >> s) & 1u) && !mbar_try_wait(full + 8 * s, (parity >> s) & 1u))
+            if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
 __device__ __forceinline__ void f4_store(const F4Args &a, int64_t m, int64_t row, float y) {
@@ -263,253 +249,275 @@ __device__ __forceinline__ void f4_store(const F4Args &a, int64_t m, int64_t row
     else static_cast<__nv_bfloat16 *>(a.Y)[m * a.N + row] = __float2bfloat16_rn(y);
 }
 
-template <int FMT, int NT, bool CLUSTER>
+template <int FMT, int NT, bool CLUSTER, bool VEC>
 __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_constant__ F4Args a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int R = f4_round(NT);
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr int R = kF4Round, PIECE = f4_piece(NT), BUF = f4_buf_bytes(NT);
+    uint8_t *smem = align1024(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_addr(smem) + kF4TableBytes + warp * (kF4Stages * kF4StageBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kF4TableBytes + kF4RingBytes);   // a round's sums are written; flag
-    volatile int *abort = reinterpret_cast<int *>(bars + 1);
-    float *seg = reinterpret_cast<float *>(smem + kF4TableBytes + kF4RingBytes + kF4BarBytes);
-    const uint32_t bar = smem_addr(bars);
+    const uint32_t ring = smem_addr(smem) + warp * (kF4Stages * kF4StageBytes);
+    const uint32_t cring = smem_addr(smem) + kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes);
+    const uint32_t full = smem_addr(smem) + f4_bar_at(NT) + warp * (kF4Stages * 8);
+    const uint32_t bar = smem_addr(smem) + f4_bar_at(NT) + kF4Warps * kF4Stages * 8;   // a round's sums are written
+    volatile int *abort = reinterpret_cast<int *>(smem + f4_bar_at(NT) + kF4Warps * kF4Stages * 8 + 8);
+    float *seg = reinterpret_cast<float *>(smem + f4_seg_at(NT));
+    if (lane < kF4Stages) mbar_init(full + 8 * lane, 1);
     if (threadIdx.x == 0) {
         mbar_init(bar, kF4Warps);
         *abort = 0;
-        fence_barrier_init();
     }
+    fence_barrier_init();
+    if (lane == 0) {
+        tma_prefetch_desc(&a.codes);
+        if (VEC) tma_prefetch_desc(&a.scales);
+    }
+    __syncthreads();
+    // A kernel behind this one may be set up while this one runs; both touch global memory only after
+    // the kernel before them has ended.
+    griddep_launch_dependents();
+    griddep_wait();
+
     const int wk = CLUSTER ? kF4Warps : a.wk, tg = kF4Warps / wk;
     const int kw = CLUSTER ? warp : warp % wk, tw = CLUSTER ? 0 : warp / wk;
     const int nch = CLUSTER ? a.nch : 1, passes = CLUSTER ? a.passes : 1;
     const int rank = CLUSTER ? (int)cluster_ctarank() : 0;
     const int ncl = gridDim.x / nch, cl = blockIdx.x / nch;
-    const int groups = (int)((a.N + s4::kStepRows * tg - 1) / (s4::kStepRows * tg));
+    const int groups = (int)((a.N + kF4StepRows * tg - 1) / (kF4StepRows * tg));
     const int mine = (groups - cl + ncl - 1) / ncl;        // tile groups cl, cl + ncl, ...
     const int64_t m0 = (int64_t)blockIdx.y * kF4Tokens;
     const int mn = (int)min((int64_t)kF4Tokens, a.M - m0);
-    // the row's slices, spread evenly over passes x CTAs: this CTA has slices lo .. lo + n - 1 of a pass
+    // the row's slices, spread evenly over passes x CTAs
     const int parts = passes * nch, sq = a.nsl / parts, srem = a.nsl % parts;
-    auto slice_of = [&](int pass) {                         // this warp's slice in a pass, -1 for none
-        const int p = pass * nch + rank, n = sq + (p < srem ? 1 : 0);
-        return kw < n ? p * sq + min(p, srem) + kw : -1;
-    };
-    const int seg_len = CLUSTER ? f4_seg_tiles(NT) : mine;
 
-    // the copies run ahead of the products over round, pass and segment borders
-    const uint32_t rb = (uint32_t)a.K / 2, sb = (uint32_t)a.kbs * 4;
-    const int row_step = ncl * tg * s4::kStepRows;
-    F4Lane ln;
-    ln.dst = s4::code_off(lane >> 3, lane & 7);
-    ln.row0 = tw * s4::kStepRows;
-    int is0 = 0, ii = 0, ip = 0, ps = 0, isl = slice_of(0); // issue position: segment, tile in it, pass
-    int64_t irow = (int64_t)cl * tg * s4::kStepRows;        // first row of the CTA's tile group
-    auto set_lane = [&]() {
-        const bool in = isl >= 0 && isl * s4::kStepK + 32 * (lane & 7) < a.K;
-        ln.code_off = (ln.row0 + (lane >> 3)) * rb + (in ? (uint32_t)(isl * 128 + (lane & 7) * 16) : 0u);
-        ln.scale_off = (ln.row0 + lane) * sb + (uint32_t)max(isl, 0) * 16;
-        ln.bytes = in ? 16 : 0;
-    };
-    set_lane();
-    auto issue = [&]() {
-        if (isl >= 0 && ii < min(seg_len, mine - is0)) {
-            f4_issue(a, ring + ps * kF4StageBytes, a.codes + irow * rb, a.absmax + irow * a.kbs,
-                     (int)min(a.N - irow, (int64_t)256) - ln.row0, ln, isl, lane);
-            irow += row_step;
-            ++ii;
-        }
-        s4::cp_commit();
-        ps = ps + 1 == kF4Stages ? 0 : ps + 1;
-        while (CLUSTER && is0 < mine && (isl < 0 || ii == min(seg_len, mine - is0))) {   // next pass or segment
-            if (++ip == passes) {
-                ip = 0;
-                is0 += seg_len;
-            }
-            ii = 0;
-            isl = slice_of(ip);
-            irow = ((int64_t)cl + (int64_t)is0 * ncl) * s4::kStepRows;
-            set_lane();
-        }
-    };
+    // this lane's codes of block b in a stage: matrix rows g and g + 8 are rows 2 g and 2 g + 1 of the
+    // tile, so that a wavefront of 16 lanes reads 32 bytes of four rows of one parity, which the
+    // swizzle keeps in different banks (row 2 g + 1: the other 16 bytes, 128 further)
+    const uint8_t *at[4];
 #pragma unroll
-    for (int i = 0; i < kF4Stages - 1; ++i) issue();
+    for (int b = 0; b < 4; ++b)
+        at[b] = smem + warp * (kF4Stages * kF4StageBytes) + g * 256 + ((b ^ (g & 3)) << 5) + t * 8;
+    const int at_odd = 128 + ((t & 2) ? -16 : 16);
+    const uint8_t *sc = smem + kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes) + g * 32;
+    // pieces of a buffer: [tiles side by side][tile of the round][warp along the row]
+    uint8_t *mypiece = smem + kF4SumAt + (tw * R * wk + kw) * PIECE;
+    int put[4];                                             // this lane's places: tokens 2 t, 2 t + 1, rows 2 g, 2 g + 1
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put[e] = 4 * f4_sum_at(2 * t + (e & 1), 2 * g + (e >> 1));
 
-    if (from_table<FMT>(1)) {
-        for (int i = threadIdx.x; i < 256 * 8; i += kF4Threads) {
-            const uint32_t v = code_f16<FMT>(i >> 7) | (code_f16<FMT>((i >> 3) & 15) << 16);
-            *reinterpret_cast<uint4 *>(smem + (i >> 3) * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
-        }
-    }
-    __syncthreads();
-    uint32_t at[4];                                         // this lane's codes of block b in a stage
-#pragma unroll
-    for (int b = 0; b < 4; ++b) at[b] = ring + g * 128 + t * 8 + ((b ^ (g & 3)) << 5);
-    const uint32_t sc_a = ring + s4::kCodeBytes + g * 16;
-    // pieces of a round: [tiles side by side][tile of the round][warp along the row]
-    const int piece0 = tw * R * wk + kw;                    // this warp's, plus wk per tile of the round
-    constexpr int kBufPieces = kF4Warps * R;
-    uint8_t *put[4];                                        // this lane's places in piece 0: tokens 2 t, 2 t + 1, rows g, g + 8
-#pragma unroll
-    for (int i = 0; i < 4; ++i) put[i] = smem + f4_hole<NT>(0, f4_sum_at(2 * t + (i & 1), g + 8 * (i >> 1)));
-    // Adds a finished round over the warps, in warp order: tiles i0 .. i0 + rn - 1 of segment s0, written as
-    // round number `round`. The warps take turns at the start of the element range.
-    auto add_round = [&](int round, int i0, int rn, bool first) {
-        if (!mbar_wait(bar, round & 1, abort)) return;
-        // element 16 m + r of tile ti; the warps take turns at the start of the range
-        for (int e = ((warp + 5 * round) & (kF4Warps - 1)) * 32 + lane; e < tg * R * 128 * NT; e += kF4Threads) {
+    // Adds round `round` (tiles i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
+    // `act` warps that have a slice, in warp order.
+    auto add_round = [&](int round, int i0, int sg, int rn, int act, bool first) {
+        if (!f4_wait(bar, round & 1, abort)) return;
+        const uint8_t *buf = smem + kF4SumAt + (round & 1) * BUF;
+        for (int e = threadIdx.x; e < tg * R * 128 * NT; e += kF4Threads) {
             const int ti = e / (128 * NT), o = e & (128 * NT - 1), m = o >> 4, r = o & 15;
             const int i = ti & (R - 1);                     // ti = (tile side by side) * R + (tile of the round)
             if (i >= rn || m >= mn) continue;
-            const uint8_t *src = smem + f4_hole<NT>((round & 1) * kBufPieces + ti * wk, f4_sum_at(m, r));
+            const uint8_t *src = buf + ti * wk * PIECE + 4 * f4_sum_at(m, r);
             float y = 0.0f;
-#pragma unroll 16
-            for (int w = 0; w < wk; ++w) y += *reinterpret_cast<const float *>(src + w * (NT * 1024));
+            if (act == kF4Warps) {
+                float v[kF4Warps];
+#pragma unroll
+                for (int w = 0; w < kF4Warps; ++w) v[w] = *reinterpret_cast<const float *>(src + w * PIECE);
+#pragma unroll
+                for (int w = 0; w < kF4Warps; ++w) y += v[w];
+            } else {
+#pragma unroll 4
+                for (int w = 0; w < act; ++w) y += *reinterpret_cast<const float *>(src + w * PIECE);
+            }
             if (CLUSTER) {
-                float *dst = seg + (i0 + i) * (128 * NT) + o;
+                float *dst = seg + (sg + i) * (128 * NT) + o;
                 *dst = first ? y : *dst + y;
             } else {
-                const int64_t row = (int64_t)(cl + (i0 + i) * ncl) * (tg * s4::kStepRows) + (ti / R) * s4::kStepRows + r;
-                if (row < a.N) f4_store(a, m0 + m, row, y);
+                const int row = (cl + (i0 + i) * ncl) * (tg * kF4StepRows) + (ti / R) * kF4StepRows + r;
+                if (row < (int)a.N) f4_store(a, m0 + m, row, y);
             }
         }
     };
-    int cs = 0, round = 0;
+
+    const int seg_len = CLUSTER ? f4_seg_tiles(NT) : mine;
+    uint32_t xb[NT][32];
+    float up[NT][2];
+    uint32_t parity = 0, flying = 0;                        // per stage: phase to wait for; copies under way
+    int round = 0, sl = -1, act = 0;
+    bool dead = false;                                      // a wait ran out
+    // Fills stage i % S with tile i (lane 0; the constants by every lane where TMA cannot)
+    auto fill = [&](int i) {
+        const int st = i & (kF4Stages - 1), row0 = ((cl + i * ncl) * tg + tw) * kF4StepRows;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(full + 8 * st, kF4StageBytes + (VEC ? kF4ScaleBytes : 0));
+            tma_load_2d(ring + st * kF4StageBytes, &a.codes, full + 8 * st, sl * 128, row0);
+            if (VEC) tma_load_2d(cring + st * kF4ScaleBytes, &a.scales, full + 8 * st, sl * 4, row0);
+        }
+        if (!VEC) f4_scales(a, cring + st * kF4ScaleBytes, row0, sl, lane);
+        flying |= 1u << st;
+    };
+
     for (int s0 = 0; s0 < mine; s0 += seg_len) {
-        const int n = min(seg_len, mine - s0);
+        const int s1 = min(mine, s0 + seg_len);
         for (int pass = 0; pass < passes; ++pass) {
-            const int sl = slice_of(pass);
-            uint32_t xb[NT][32];
-            float up[NT][2];
-            if (sl >= 0) {
-                // handed over in the places of this warp's own sums: 512 bytes for each of four tokens
-                auto stage = [&](int m, int u) {
-                    const int p = (m >> 1) * kBufPieces + (NT == 1 ? (m & 1) * wk : 0);
-                    return reinterpret_cast<uint4 *>(smem + f4_hole<NT>(p + piece0, 4 * u + (NT == 1 ? 0 : (m & 1) * 128)));
-                };
+            // tiles whose copies may run ahead: with several passes, this segment's only
+            const int ahead = passes > 1 ? s1 : mine;
+            if (passes > 1 || s0 == 0) {
+                const int p = pass * nch + rank;
+                act = sq + (p < srem ? 1 : 0);
+                sl = kw < act && !dead ? p * sq + min(p, srem) + kw : -1;
+                if (sl >= 0) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    f4_tokens<FMT>(a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * s4::kStepK, lane, stage, xb[nt],
-                                   up[nt][0], up[nt][1]);
-            }
-            for (int i0 = 0; i0 < n; i0 += R, ++round) {
-                const int rn = min(R, n - i0);
-                for (int i = 0; i < rn; ++i) {
-                    const uint32_t po = ((round & 1) * kBufPieces + piece0 + i * wk) * (NT * 1024);
-                    if (sl < 0) {
-                        if (i == 0 && i0 > 0) add_round(round - 1, i0 - R, R, pass == 0);
-                        for (int e = lane; e < 128 * NT; e += 32) *reinterpret_cast<float *>(smem + po + f4_hole<NT>(0, e)) = 0.0f;
-                        continue;
+                    for (int i = 0; i < kF4Stages; ++i) {
+                        if (s0 + i < ahead) fill(s0 + i);
+                        if ((i & (R - 1)) == R - 1) cp_commit();
                     }
-                    float acc[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-                    s4::cp_wait<kF4Stages - 2>();
-                    __syncwarp();
-                    issue();
-                    const uint32_t so = cs * kF4StageBytes;
-                    cs = cs + 1 == kF4Stages ? 0 : cs + 1;
-                    const float4 f0 = s4::lds128f(sc_a + so), f1 = s4::lds128f(sc_a + so + 128);
-                    const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint2 u = s4::lds64(at[b] + so), v = s4::lds64(at[b] + so + 8 * 128);
-                        float c[NT][4];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t p[4], q[4];
-                            decode<FMT>(a, smem, lane * 4, j, j ? u.y : u.x, p);
-                            decode<FMT>(a, smem, lane * 4, j, j ? v.y : v.x, q);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t *x = xb[nt] + 8 * b + 4 * j;
-                                if (j == 0) mma_f16_first(c[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
-                                else mma_f16(c[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
-                            }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t *x = xb[nt] + 8 * b + 4 * j;
-                                mma_f16(c[nt], p[2], q[2], p[3], q[3], x[2], x[3]);
-                            }
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            acc[nt][0] = fmaf(c0[b], c[nt][0], acc[nt][0]);
-                            acc[nt][1] = fmaf(c0[b], c[nt][1], acc[nt][1]);
-                            acc[nt][2] = fmaf(c1[b], c[nt][2], acc[nt][2]);
-                            acc[nt][3] = fmaf(c1[b], c[nt][3], acc[nt][3]);
-                        }
-                    }
-                    // the round before, whose buffer the next round needs: a step after it ended
-                    if (i == 0 && i0 > 0) add_round(round - 1, i0 - R, R, pass == 0);
+                    // handed over in the places of this warp's own sums (a pass before has been added)
+                    auto stage = [&](int m, int u) {
+                        return reinterpret_cast<uint4 *>(mypiece + (m >> 1) * BUF + (m & 1) * (wk * PIECE) + 16 * u);
+                    };
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (8 * nt + 2 * t + (e & 1) < mn)
-                                *reinterpret_cast<float *>(put[e] + po + nt * 1024) = acc[nt][e] * up[nt][e & 1];
+                        f4_tokens<FMT>(a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * kF4StepK, lane, stage, xb[nt],
+                                       up[nt][0], up[nt][1]);
                 }
-                __syncwarp();
+            }
+            for (int i0 = s0; i0 < s1; i0 += R, ++round) {
+                uint8_t *piece = mypiece + (round & 1) * BUF;
+                if (sl < 0 && i0 > s0) add_round(round - 1, i0 - R, i0 - R - s0, R, act, pass == 0);
+                if (sl >= 0) {
+                    cp_wait<1>();
+                    if (!VEC) __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        if (i0 + i >= s1) break;
+                        const int st = (i0 + i) & (kF4Stages - 1), so = st * kF4StageBytes;
+                        if (!f4_wait(full + 8 * st, (parity >> st) & 1u, abort)) {
+                            f4_drain(full, flying, parity);   // the CTA goes on without this warp's slices
+                            dead = true;
+                            sl = -1;
+                            break;
+                        }
+                        parity ^= 1u << st;
+                        flying &= ~(1u << st);
+                        const float4 f0 = *reinterpret_cast<const float4 *>(sc + st * kF4ScaleBytes);
+                        const float4 f1 = *reinterpret_cast<const float4 *>(sc + st * kF4ScaleBytes + 16);
+                        const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
+                        float acc[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint2 u = *reinterpret_cast<const uint2 *>(at[b] + so);
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at[b] + (so + at_odd));
+                            float cc[NT][4];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                uint32_t p[4], q[4];
+                                decode<FMT>(a, j ? u.y : u.x, p);
+                                decode<FMT>(a, j ? v.y : v.x, q);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const uint32_t *x = xb[nt] + 8 * b + 4 * j;
+                                    if (j == 0) mma_f16_first(cc[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
+                                    else mma_f16(cc[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const uint32_t *x = xb[nt] + 8 * b + 4 * j;
+                                    mma_f16(cc[nt], p[2], q[2], p[3], q[3], x[2], x[3]);
+                                }
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                acc[nt][0] = fmaf(c0[b], cc[nt][0], acc[nt][0]);
+                                acc[nt][1] = fmaf(c0[b], cc[nt][1], acc[nt][1]);
+                                acc[nt][2] = fmaf(c1[b], cc[nt][2], acc[nt][2]);
+                                acc[nt][3] = fmaf(c1[b], cc[nt][3], acc[nt][3]);
+                            }
+                        }
+                        // the round before, whose buffer the next round needs: a step after it ended
+                        if (i == 0 && i0 > s0) add_round(round - 1, i0 - R, i0 - R - s0, R, act, pass == 0);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (8 * nt + 2 * t + (e & 1) < mn)
+                                    *reinterpret_cast<float *>(piece + i * wk * PIECE + nt * 512 + put[e]) = acc[nt][e] * up[nt][e & 1];
+                    }
+                }
+                __syncwarp();                          // the stages have been read, the sums written
                 if (lane == 0) mbar_arrive(bar);
+                if (sl >= 0) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (i0 + i + kF4Stages < ahead) fill(i0 + i + kF4Stages);
+                    cp_commit();
+                }
             }
-            if (n > 0) {
-                const int last = (n - 1) / R * R;
-                add_round(round - 1, last, n - last, pass == 0);
-            }
+            const int last = s0 + (s1 - s0 - 1) / R * R;
+            add_round(round - 1, last, last - s0, s1 - last, act, pass == 0);
             if (CLUSTER) __syncthreads();              // the buffers are free for the next pass's hand-over
         }
         if (CLUSTER) {
             // the CTAs' sums in rank order; the CTAs take turns over the segment's elements
             cluster_sync();
             const uint32_t base = smem_addr(seg);
-            for (int e = rank * kF4Threads + threadIdx.x; e < n * 16 * mn; e += nch * kF4Threads) {
-                const int i = e / (16 * mn), o = e - i * 16 * mn;
+            for (int e = rank * kF4Threads + threadIdx.x; e < (s1 - s0) * 128 * NT; e += nch * kF4Threads) {
+                const int i = e / (128 * NT), o = e & (128 * NT - 1), m = o >> 4;
+                const int64_t row = (int64_t)(cl + (s0 + i) * ncl) * kF4StepRows + (o & 15);
+                if (m >= mn || row >= a.N) continue;
                 float y = 0.0f;
-                for (int c = 0; c < nch; ++c) y += ld_cluster_f32(map_to_rank(base + 4 * (i * (128 * NT) + o), c));
-                const int64_t row = (int64_t)(cl + (s0 + i) * ncl) * s4::kStepRows + (o & 15);
-                if (row < a.N) f4_store(a, m0 + (o >> 4), row, y);
+                for (int c = 0; c < nch; ++c) y += ld_cluster_f32(map_to_rank(base + 4 * e, c));
+                f4_store(a, m0 + m, row, y);
             }
             cluster_sync();                            // before the next segment's sums, or the exit
         }
     }
-    s4::cp_wait<0>();
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool CLUSTER, bool VEC>
 cudaError_t f4_launch(const F4Args &a, int64_t groups, cudaStream_t st) {
-    const bool cluster = a.nch > 1 || a.passes > 1;
-    auto kernel = cluster ? k_fmt4_linear<FMT, NT, true> : k_fmt4_linear<FMT, NT, false>;
+    auto kernel = k_fmt4_linear<FMT, NT, CLUSTER, VEC>;
+    constexpr int smem = f4_smem(NT, CLUSTER);
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)a.nch;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)a.nch;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(kF4Threads);
-    cfg.dynamicSmemBytes = f4_smem(cluster);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = cluster ? 1 : 0;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    cfg.attrs = CLUSTER ? at : at + 1;
+    cudaError_t e = set_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     // clusters that run at once: fewer than SMs / size where the chip's SM groups do not divide
     int most = num_sms();
-    if (cluster) {
+    if (CLUSTER) {
         static std::atomic<int> active[kF4MaxCluster + 1];
         most = active[a.nch].load(std::memory_order_relaxed);
         if (most == 0) {
             cfg.gridDim = dim3((unsigned)a.nch);
+            cfg.numAttrs = 1;
             if ((e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg)) != cudaSuccess) return e;
             if (most < 1) most = 1;
             active[a.nch].store(most, std::memory_order_relaxed);
         }
     }
+    cfg.numAttrs = (CLUSTER ? 1 : 0) + (profiling_launches() ? 0 : 1);
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(groups, most) * a.nch), (unsigned)ceil_div(a.M, (int64_t)kF4Tokens));
     QNF4_LAUNCH("k_fmt4_linear", st, e = cudaLaunchKernelEx(&cfg, kernel, a));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int FMT, int NT>
+cudaError_t f4_launch_form(const F4Args &a, int64_t groups, cudaStream_t st) {
+    if (a.nch > 1 || a.passes > 1)
+        return a.vec_scales ? f4_launch<FMT, NT, true, true>(a, groups, st) : f4_launch<FMT, NT, true, false>(a, groups, st);
+    return a.vec_scales ? f4_launch<FMT, NT, false, true>(a, groups, st) : f4_launch<FMT, NT, false, false>(a, groups, st);
+}
+
 template <int FMT>
 cudaError_t f4_launch_tiles(const F4Args &a, int64_t groups, cudaStream_t st) {
-    const int64_t m = a.M < kF4Tokens ? a.M : kF4Tokens;
-    return m <= 8 ? f4_launch<FMT, 1>(a, groups, st) : f4_launch<FMT, 2>(a, groups, st);
+    return a.M <= 8 ? f4_launch_form<FMT, 1>(a, groups, st) : f4_launch_form<FMT, 2>(a, groups, st);
 }
 
 }  // namespace
@@ -518,14 +526,16 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
                                int64_t cols, qlora_fmt4 f, void *Y, bool y_f32, cudaStream_t st) {
     F4Args a;
     a.X = X;
-    a.codes = codes;
+    if (!make_map(&a.codes, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)cols / 2, (uint64_t)rows, (uint64_t)cols / 2, 128,
+                  kF4StepRows, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
     a.absmax = absmax;
     a.Y = Y;
     a.M = M;
     a.N = rows;
     a.K = (int)cols;
     a.kbs = (int)(cols / kBlock1);
-    a.nsl = (int)ceil_div(cols, s4::kStepK);
+    a.nsl = (int)ceil_div(cols, kF4StepK);
     a.y_f32 = y_f32;
     a.two2 = 4;
     a.two4 = 16;
@@ -534,18 +544,20 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
     a.vec_scales = a.kbs % 4 == 0 && aligned16(absmax);
     // Int4 operands are m 2^-16; an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7)
     a.factor = f == QLORA_FMT4_INT4 ? 65536.0f / 7.0f : f == QLORA_FMT4_FP4_E2M1 ? 1.0f / 6.0f : 0.0625f;
-    const int sms = num_sms();
+    if (a.vec_scales && !make_map(&a.scales, absmax, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)a.kbs, (uint64_t)rows,
+                                  (uint64_t)a.kbs * 4, 4, kF4StepRows, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
     // CTAs along a row: enough for a slice per warp, more while there are fewer tiles than SMs
-    const int64_t tiles = ceil_div(rows, (int64_t)s4::kStepRows);
+    const int64_t tiles = ceil_div(rows, (int64_t)kF4StepRows);
     int64_t nch = ceil_div(a.nsl, kF4Warps);
-    while (nch < kF4MaxCluster && tiles * (nch + 1) <= sms && a.nsl >= 4 * (nch + 1)) ++nch;
+    while (nch < kF4MaxCluster && tiles * (nch + 1) <= num_sms() && a.nsl >= 4 * (nch + 1)) ++nch;
     if (nch > kF4MaxCluster) nch = kF4MaxCluster;
     a.nch = (int)nch;
     a.passes = (int)ceil_div(a.nsl, nch * kF4Warps);
     a.wk = kF4Warps;
     if (nch == 1)
         while (a.wk > 1 && a.wk / 2 >= a.nsl) a.wk /= 2;
-    const int64_t groups = ceil_div(rows, (int64_t)s4::kStepRows * (kF4Warps / a.wk));
+    const int64_t groups = ceil_div(rows, (int64_t)kF4StepRows * (kF4Warps / a.wk));
     switch (f) {
         case QLORA_FMT4_INT4: return f4_launch_tiles<QLORA_FMT4_INT4>(a, groups, st);
         case QLORA_FMT4_FP4_E2M1: return f4_launch_tiles<QLORA_FMT4_FP4_E2M1>(a, groups, st);

@@ -396,7 +396,7 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
  * Every output is a sum in a fixed order. A NaN or infinity in X or absmax reaches the
  * outputs whose sums hold it, as in the formula. One kernel launch; no workspace.
  * QLORA_ERR_INVALID_ARG for a null or misaligned pointer, an unknown format or dtype;
- * QLORA_ERR_UNSUPPORTED_SHAPE for sizes outside the rules above (or rows above 2^31, cols
+ * QLORA_ERR_UNSUPPORTED_SHAPE for sizes outside the rules above (or rows above 2^30, cols
  * above 2^27).
  */
 qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
