@@ -102,6 +102,12 @@ _SIGS = {
     "qlora_fmt4_linear_fwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
                                              ctypes.c_void_p]),
+    "qlora_moe_fwd_workspace": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                  ctypes.c_int]),
+    "qlora_moe_fwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                     ctypes.POINTER(_Tensor), ctypes.POINTER(_Tensor), ctypes.POINTER(_Tensor), ctypes.c_int,
+                                     ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_size_t, ctypes.c_void_p]),
     "qlora_launch_count": (ctypes.c_ulonglong, []),
     "qlora_profile_enable": (None, [ctypes.c_int]),
     "qlora_profile_read": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
@@ -472,6 +478,43 @@ def qlora_linear_fwd_grouped(items, ws: torch.Tensor | None = None, stream=None)
     _check(L.qlora_linear_fwd_grouped(M, n, descs, _ptr(wsb), wsn, _stream(stream)), "qlora_linear_fwd_grouped")
     _hold(stream, wsb)
     return outs
+
+
+def qlora_moe_fwd_workspace(T: int, d: int, f: int, E: int, k: int) -> int:
+    """Workspace bytes of qlora_moe_fwd for T tokens of width d, E experts of hidden width f, k per token."""
+    return int(lib().qlora_moe_fwd_workspace(T, d, f, E, k))
+
+
+def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF4Tensor, down: NF4Tensor, k: int,
+                  renorm: bool = True, Y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Mixture-of-experts layer for a few tokens X (bf16 [T, d]) with NF4 experts: router [E, d] (bf16 or
+    fp32), gate and up [E f, d], down [E d, f]. Returns (Y bf16 [T, d], experts int32 [T, k], weights fp32
+    [T, k])."""
+    if X.dim() != 2 or X.dtype != torch.bfloat16:
+        raise ValueError("qlora_moe_fwd: X must be a bf16 [T, d] tensor")
+    rdt = _DTYPES.get(router.dtype)
+    if rdt is None or router.dim() != 2 or router.shape[1] != X.shape[1]:
+        raise ValueError("qlora_moe_fwd: router must be a bf16 or fp32 [E, d] tensor")
+    T, d = X.shape
+    E, f, dev = router.shape[0], down.cols, X.device
+    if gate.cols != d:
+        raise ValueError("qlora_moe_fwd: gate must have d columns")
+    if Y is None:
+        Y = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+    elif Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous():
+        raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
+    _same_device("qlora_moe_fwd", dev, router, Y, gate.codes, up.codes, down.codes, *(() if ws is None else (ws,)))
+    Xc, rc = X.contiguous(), router.contiguous()
+    experts = torch.empty(T, k, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+    L = lib()
+    wsb, wsn = _workspace(L.qlora_moe_fwd_workspace(T, d, f, E, k), dev, ws)
+    tg, tu, td = gate.ctype(), up.ctype(), down.ctype()
+    _launch("qlora_moe_fwd", L.qlora_moe_fwd, dev, stream, Xc.data_ptr(), T, rc.data_ptr(), rdt, E, ctypes.byref(tg),
+            ctypes.byref(tu), ctypes.byref(td), k, int(renorm), Y.data_ptr(), experts.data_ptr(), weights.data_ptr(),
+            0 if wsb is None else wsb.data_ptr(), wsn)
+    _hold(stream, Xc, rc, wsb)
+    return Y, experts, weights
 
 
 def qlora_linear_bwd(X: torch.Tensor, dY: torch.Tensor, W: NF4Tensor, A: torch.Tensor | None,

@@ -340,6 +340,29 @@ qlora_status qlora_fmt4_linear_fwd(const void *X, int64_t M, const uint8_t *code
                                         ydt == QLORA_F32, static_cast<cudaStream_t>(stream)));
 }
 
+size_t qlora_moe_fwd_workspace(int64_t T, int64_t d, int64_t f, int64_t E, int k) {
+    return moe_shape_ok(T, d, f, E, k) ? moe_workspace_bytes(T, d, f, E, k) : 0;
+}
+
+qlora_status qlora_moe_fwd(const void *X, int64_t T, const void *router, qlora_dtype rdt, int64_t E,
+                           const qlora_nf4_tensor *gate, const qlora_nf4_tensor *up, const qlora_nf4_tensor *down, int k,
+                           int renorm, void *Y, int32_t *experts, float *weights, void *ws, size_t ws_bytes,
+                           qlora_stream_t stream) {
+    if (!X || !router || !Y || !aligned16(X) || !aligned16(router) || !aligned16(Y) || (rdt != QLORA_F32 && rdt != QLORA_BF16) ||
+        !tensor_ok(gate) || !tensor_ok(up) || !tensor_ok(down) || (reinterpret_cast<uintptr_t>(experts) & 3u) ||
+        (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return QLORA_ERR_INVALID_ARG;
+    for (const qlora_nf4_tensor *t : {gate, up, down})
+        if (reinterpret_cast<uintptr_t>(t->scale8) & 3u) return QLORA_ERR_INVALID_ARG;
+    const int64_t d = gate->cols, f = down->cols;
+    if (!moe_shape_ok(T, d, f, E, k) || gate->rows != E * f || up->rows != E * f || up->cols != d || down->rows != E * d)
+        return QLORA_ERR_UNSUPPORTED_SHAPE;
+    if (!ws || ws_bytes < moe_workspace_bytes(T, d, f, E, k) || !aligned16(ws)) return QLORA_ERR_WORKSPACE;
+    return from_cuda(launch_moe(static_cast<const __nv_bfloat16 *>(X), T, router, rdt == QLORA_F32, view_of(gate), view_of(up),
+                                view_of(down), d, f, E, k, renorm != 0, static_cast<__nv_bfloat16 *>(Y), experts, weights, ws,
+                                static_cast<cudaStream_t>(stream)));
+}
+
 qlora_status qlora_get_device_status(qlora_stream_t stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QLORA_ERR_CUDA;
     unsigned int bits = 0, zero = 0;

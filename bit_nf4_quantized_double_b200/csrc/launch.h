@@ -26,6 +26,12 @@ cudaError_t launch_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
                                 __nv_bfloat16 *out, cudaStream_t st);
 cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t *codes, const float *absmax, int64_t rows,
                                int64_t cols, qlora_fmt4 f, void *Y, bool y_f32, cudaStream_t st);
+// Mixture-of-experts layer (moe.cu): T tokens of width D, E experts of hidden width F, k per token.
+bool moe_shape_ok(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k);
+size_t moe_workspace_bytes(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k);
+cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bool router_f32, const NF4View &gate,
+                       const NF4View &up, const NF4View &down, int64_t D, int64_t F, int64_t E, int k, bool renorm,
+                       __nv_bfloat16 *Y, int *experts, float *weights, void *ws, cudaStream_t st);
 cudaError_t launch_adamw(float *theta, const float *g, float *m, float *v, int64_t n, float lr, float b1, float b2,
                          float eps, float wd, int64_t step, __nv_bfloat16 *out_bf16, cudaStream_t st);
 cudaError_t launch_prefetch(const void *ptr, size_t bytes, bool to_device, cudaStream_t st);

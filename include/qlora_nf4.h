@@ -224,6 +224,41 @@ size_t qlora_linear_fwd_grouped_workspace(int64_t M, int count, const qlora_line
 qlora_status qlora_linear_fwd_grouped(int64_t M, int count, const qlora_linear_desc *d, void *ws,
                                       size_t ws_bytes, qlora_stream_t stream);
 
+/*
+ * A mixture-of-experts layer whose experts are stored weights, for the few tokens of a decode
+ * step (the page gives the stored weight and its product; the layer around them is the usual
+ * one):
+ *   logits[t, e] = sum_i X[t, i] router[e, i];
+ *   experts[t, :] = the k experts with the largest logits, largest first, ties to the lower;
+ *   weights[t, j] = softmax(logits[t, :]) at experts[t, j], divided by the token's k such
+ *                   values' sum when renorm != 0;
+ *   Y[t] = sum_j weights[t, j] down_e (silu(gate_e x_t) * (up_e x_t)),  e = experts[t, j],
+ *   silu(z) = z / (1 + exp(-z)).
+ *   X        bf16 [T, d], 1 <= T <= 64.
+ *   router   fp32 or bf16 [E, d] by rdt, 1 <= E <= 256.
+ *   gate, up stored tensors of E * f rows and d columns, down of E * d rows and f columns: the
+ *            experts' rows one after the other (quantise the stacked matrix as one tensor);
+ *            scale8 4-byte aligned. d and f are multiples of 64, at most 65536.
+ *   k        1 <= k <= min(E, 16).
+ *   Y        bf16 [T, d]. experts int32 [T, k] and weights fp32 [T, k] receive the choice, or
+ *            are NULL.
+ *   ws       device workspace of qlora_moe_fwd_workspace() bytes (0 for shapes outside these
+ *            rules). Calls that may run at the same time need a workspace each.
+ * Logits are sums in fp64, so the choice does not depend on the order of a sum. The products
+ * use the codebook and the activations as fp16 (2^-12 relative; activations scaled by powers of
+ * two so that nothing overflows) and fp32 sums, the hidden values likewise; Y is rounded once.
+ * Every output is a sum in a fixed order. A NaN logit counts as the largest; the outputs of a
+ * token with a NaN or an infinity are what the formula gives for the experts chosen that way.
+ * Two launches; the second is cooperative (one CTA per SM, two bounded grid barriers:
+ * QLORA_ERR_TIMEOUT in the status word if one runs out). QLORA_ERR_CUDA where the device
+ * cannot hold all its CTAs at once.
+ */
+size_t qlora_moe_fwd_workspace(int64_t T, int64_t d, int64_t f, int64_t E, int k);
+qlora_status qlora_moe_fwd(const void *X, int64_t T, const void *router, qlora_dtype rdt, int64_t E,
+                           const qlora_nf4_tensor *gate, const qlora_nf4_tensor *up, const qlora_nf4_tensor *down, int k,
+                           int renorm, void *Y, int32_t *experts, float *weights, void *ws, size_t ws_bytes,
+                           qlora_stream_t stream);
+
 /* Synchronises `stream`, returns the first condition recorded on the current
  * device since the last call (QLORA_OK if none) and clears it. */
 qlora_status qlora_get_device_status(qlora_stream_t stream);
