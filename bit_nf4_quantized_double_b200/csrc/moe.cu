@@ -21,9 +21,9 @@
 // lane; mma.sync m16n8k16 sums a 64-block, fp32 arithmetic applies its constant
 // c = scale8 (scale2 / 127) + offset. The warps' sums of a tile are added in warp order.
 //
-// Roundings besides fp32: the codebook to fp16 (2^-12 relative; bf16 would be 2^-9, as much as
+// Roundings besides fp32: the codebook to fp16 (2^-11 relative; bf16 would be 2^-8, as much as
 // the output's own), the tokens to fp16 after scaling by a power of two per token and 256 inputs
-// (exact within 2^-31 of the largest), silu(g) u to fp16 likewise (2^-12).
+// (exact within 2^-31 of the largest), silu(g) u to fp16 likewise (2^-11).
 #include <cuda_fp16.h>
 
 #include <algorithm>

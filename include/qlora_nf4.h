@@ -245,7 +245,7 @@ qlora_status qlora_linear_fwd_grouped(int64_t M, int count, const qlora_linear_d
  *   ws       device workspace of qlora_moe_fwd_workspace() bytes (0 for shapes outside these
  *            rules). Calls that may run at the same time need a workspace each.
  * Logits are sums in fp64, so the choice does not depend on the order of a sum. The products
- * use the codebook and the activations as fp16 (2^-12 relative; activations scaled by powers of
+ * use the codebook and the activations as fp16 (2^-11 relative; activations scaled by powers of
  * two so that nothing overflows) and fp32 sums, the hidden values likewise; Y is rounded once.
  * Every output is a sum in a fixed order. A NaN logit counts as the largest; the outputs of a
  * token with a NaN or an infinity are what the formula gives for the experts chosen that way.
