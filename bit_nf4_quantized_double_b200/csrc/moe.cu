@@ -14,12 +14,15 @@
 // share of the weighted sums. The chosen experts' codes, 0.516 bytes per weight, bound it; the
 // copies of the first down tiles run while the CTA waits at the first barrier.
 //
-// Products. A warp holds the tokens of a job (an expert's tokens, at most 16) for one slice of
-// 256 inputs in registers and takes tiles of 16 weight rows through its own ring of stages: eight
-// gate and the eight up rows of the same outputs, or 16 down rows. A code byte becomes an fp16
-// pair by one permute (address = byte * 256 + lane * 4) and one load from a table replicated per
-// lane; mma.sync m16n8k16 sums a 64-block, fp32 arithmetic applies its constant
-// c = scale8 (scale2 / 127) + offset. The warps' sums of a tile are added in warp order.
+// Products. Sixteen warps each hold the tokens of a job (an expert's tokens, at most eight) for
+// one slice of 256 inputs in registers and take tiles of 16 weight rows: eight gate and the eight
+// up rows of the same outputs, or 16 down rows. A code byte becomes an fp16 pair by one permute
+// (byte * 256 + lane * 4 + the table's address) and one load from a table replicated per lane;
+// mma.sync m16n8k16 sums a 64-block, fp32 arithmetic applies its constant. Seven more warps do
+// everything else, in step with the others by two barriers per stage of a ring of four: one
+// copies the codes (TMA), two add the sixteen warps' results in a fixed order, four turn int8
+// constants into c = scale8 (scale2 / 127) + offset. With all of it in the sixteen warps a tile took
+// about 560 instructions of a warp, 200 of them the products.
 //
 // Roundings besides fp32: the codebook to fp16 (2^-11 relative; bf16 would be 2^-8, as much as
 // the output's own), the tokens to fp16 after scaling by a power of two per token and 256 inputs
@@ -38,36 +41,47 @@ using namespace tc;
 
 namespace {
 
-constexpr int kMoeWarps = 16;
-constexpr int kMoeThreads = 32 * kMoeWarps;
+constexpr int kMoeWarps = 16;                       // that multiply
+constexpr int kMoeScalers = 4, kMoeAdders = 2;
+constexpr int kMoeHelpers = 1 + kMoeAdders + kMoeScalers;   // the copies, the sums, the block constants
+constexpr int kMoeThreads = 32 * (kMoeWarps + kMoeHelpers);
 constexpr int kMoeStages = 4;
 constexpr int kMoeStepK = 256;
-constexpr int kMoeStageBytes = 16 * 128;            // 16 rows x 256 inputs
-constexpr int kMoeScaleBytes = 16 * 16;             // per row: two words of int8 constants, two scales
-constexpr int kMoeJobTokens = 16;
+constexpr int kMoeStageBytes = kMoeWarps * 16 * 128;    // per warp 16 rows x 256 inputs
+constexpr int kMoeScaleRow = 16 * 16 + 16;          // a row's block constants, four per warp, and 16 bytes against bank conflicts
+constexpr int kMoeScaleBytes = 16 * kMoeScaleRow;   // of a stage
+constexpr int kMoeJob = 8;                          // tokens of a job
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 16;
 constexpr int kMoeMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMoeMaxJobs = kMoeMaxExperts + kMoeMaxSlots / kMoeJobTokens;
+constexpr int kMoeMaxJobs = kMoeMaxExperts + kMoeMaxSlots / 8;
 
 struct MoeJob {
     short expert, first, count, pad;                // slots order[first .. first + count - 1]
 };
 
-// Shared memory. The table's 256 rows are 256 bytes apart, 128 bytes used (a word per lane); the
-// other halves ("holes", 32 floats each) hold two buffers of the warps' sums.
-constexpr int kMoeRingAt = 65536;
-constexpr int kMoeScaleAt = kMoeRingAt + kMoeWarps * kMoeStages * kMoeStageBytes;
-constexpr int kMoeWeightAt = kMoeScaleAt + kMoeWarps * kMoeStages * kMoeScaleBytes;
-constexpr int kMoeChoiceAt = kMoeWeightAt + kMoeMaxSlots * 4;
-constexpr int kMoeOrderAt = kMoeChoiceAt + kMoeMaxSlots * 2;
-constexpr int kMoeJobAt = kMoeOrderAt + kMoeMaxSlots * 2;
-constexpr int kMoeCountAt = kMoeJobAt + kMoeMaxJobs * 8;
-constexpr int kMoeBarAt = kMoeCountAt + kMoeMaxExperts * 4;
-constexpr int kMoeSmem = 1024 + kMoeBarAt + kMoeWarps * kMoeStages * 8 + 32;
-static_assert(kMoeSmem <= 232448, "shared memory");
+// Shared memory, by absolute address of the shared window. The table's 256 rows are 256 bytes
+// apart, 128 bytes used (a word per lane); it starts at 65536, so that one permute of a code byte
+// and a constant of the lane is the address of a lookup. The other halves of its rows hold the
+// warps' sums, a buffer per stage. Below it the first stage, the constants and the lists, above
+// it the other stages.
+constexpr uint32_t kMoeTable = 65536;
+constexpr uint32_t kMoeLow = 1024;                  // the system keeps the first 1024 bytes of the window
+constexpr uint32_t kMoeHigh = 2 * 65536;
+constexpr uint32_t kMoeScaleAt = kMoeLow + kMoeStageBytes;
+constexpr uint32_t kMoeWeightAt = kMoeScaleAt + kMoeStages * kMoeScaleBytes;
+constexpr uint32_t kMoeChoiceAt = kMoeWeightAt + kMoeMaxSlots * 4;
+constexpr uint32_t kMoeOrderAt = kMoeChoiceAt + kMoeMaxSlots * 2;
+constexpr uint32_t kMoeJobAt = kMoeOrderAt + kMoeMaxSlots * 2;
+constexpr uint32_t kMoeBarAt = kMoeJobAt + kMoeMaxJobs * 8;
+constexpr int kMoeSmem = kMoeHigh + (kMoeStages - 1) * kMoeStageBytes - kMoeLow;
+static_assert(kMoeSmem <= 232448 && kMoeBarAt + 128 <= kMoeTable, "shared memory");
+
+__device__ __forceinline__ uint32_t stage_at(int st) { return st == 0 ? kMoeLow : kMoeHigh + (st - 1) * kMoeStageBytes; }
 
 struct MoeWeight {
-    CUtensorMap codes;                              // bytes [rows, cols / 2], 128-byte swizzle
+    // 128-byte swizzle. Where a row is a whole number of slices: bytes (128, rows, slices), boxes of a chunk's slices and
+    // of one less (chunks differ by at most one); else bytes (cols / 2, rows), box of one slice.
+    CUtensorMap codes, codes_less;
     const int8_t *scale8;
     const float *scale2, *offset;
 };
@@ -83,18 +97,11 @@ struct MoeArgs {
     int *experts;                                   // [T, k], or null
     float *weights;                                 // [T, k], or null
     int T, D, F, E, k, renorm;
-    int nsl1, nsl2, wk1, wk2, nck1, nck2;           // of D and F: slices, warps along a row, chunks of at most 16 slices
+    int whole1, whole2;                             // D, F are multiples of 256
+    int nsl1, nsl2, lwk1, lwk2, nck1, nck2;         // of D and F: slices, log2 of warps along a row, chunks of at most 16 slices
     float q[16];                                    // codebook
 };
 
-__device__ __forceinline__ void cp4n(uint32_t dst, const void *src, int n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -137,7 +144,7 @@ __device__ __forceinline__ float scale_f16(const float (&f)[8], uint4 &o) {
 
 // ---------------------------------------------------------------- routing
 constexpr int kRouteThreads = 256;
-constexpr int kRouteTokens = 4;                     // tokens per logits item
+constexpr int kRouteTokens = 4;                     // tokens of a CTA
 
 __device__ __forceinline__ void bf16x8(uint4 v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -148,59 +155,67 @@ __device__ __forceinline__ void bf16x8(uint4 v, float (&f)[8]) {
     }
 }
 
-// One warp per item: (expert, four tokens) logits, then (token, slice) conversions. The router is
-// E D values, a few hundred KB, so the kernel is a latency: a warp has all loads of 1024 inputs
-// under way at once.
+// A CTA per (expert, four tokens): its eight warps take 256 inputs each in turn and add their sums in warp order; then a
+// CTA per eight (token, slice) conversions. The router is a few hundred KB, so the kernel is a latency, mostly of fp64
+// additions that wait for one another: with a warp per logit it took 6 to 12 us.
 template <bool F32>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16 *X, const void *router, double *logits,
                                                              __half *xq, float *xup, unsigned *counters, int T, int D,
                                                              int E, int nsl) {
+    __shared__ double sums[kRouteTokens][kRouteThreads / 32];
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, tq = (T + kRouteTokens - 1) / kRouteTokens;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tq = (T + kRouteTokens - 1) / kRouteTokens;
     if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
-    const int items = E * tq + T * nsl;
-    for (int it = blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5); it < items; it += gridDim.x * (kRouteThreads / 32)) {
-        if (it < E * tq) {
-            const int e = it / tq, t0 = (it - e * tq) * kRouteTokens;
-            double acc[kRouteTokens];
+    if ((int)blockIdx.x >= E * tq) {
+        const int i = ((int)blockIdx.x - E * tq) * (kRouteThreads / 32) + warp, t = i / nsl, s = i - t * nsl;
+        if (t >= T) return;
+        const int k = s * kMoeStepK + 8 * lane;
+        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (k < D) bf16x8(__ldg(reinterpret_cast<const uint4 *>(X + (int64_t)t * D + k)), f);
+        uint4 o;
+        const float up = scale_f16(f, o);
+        *reinterpret_cast<uint4 *>(xq + (int64_t)t * nsl * kMoeStepK + k) = o;
+        if (lane == 0) xup[t * nsl + s] = up;
+        return;
+    }
+    const int e = (int)blockIdx.x / tq, t0 = ((int)blockIdx.x - e * tq) * kRouteTokens;
+    double acc[kRouteTokens][2];
 #pragma unroll
-            for (int i = 0; i < kRouteTokens; ++i) acc[i] = 0.0;
-#pragma unroll 4
-            for (int k = 8 * lane; k < D; k += 256) {
-                float r[8];
-                if (F32) {
-                    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(router) + (int64_t)e * D + k);
-                    const float4 a = __ldg(p), b = __ldg(p + 1);
-                    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-                    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
-                } else {
-                    bf16x8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(router) + (int64_t)e * D + k)), r);
-                }
-#pragma unroll
-                for (int i = 0; i < kRouteTokens; ++i) {
-                    if (t0 + i >= T) break;
-                    float x[8];
-                    bf16x8(__ldg(reinterpret_cast<const uint4 *>(X + (int64_t)(t0 + i) * D + k)), x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i] = fma((double)x[j], (double)r[j], acc[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kRouteTokens; ++i) {
-                if (t0 + i >= T) break;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-                if (lane == 0) logits[(int64_t)(t0 + i) * E + e] = acc[i];
-            }
+    for (int i = 0; i < kRouteTokens; ++i) acc[i][0] = acc[i][1] = 0.0;
+#pragma unroll 2
+    for (int k = 256 * warp + 8 * lane; k < D; k += 8 * kRouteThreads) {
+        float r[8];
+        if (F32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(router) + (int64_t)e * D + k);
+            const float4 a = __ldg(p), b = __ldg(p + 1);
+            r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+            r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
         } else {
-            const int c = it - E * tq, t = c / nsl, s = c - t * nsl, k = s * kMoeStepK + 8 * lane;
-            float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (k < D) bf16x8(__ldg(reinterpret_cast<const uint4 *>(X + (int64_t)t * D + k)), f);
-            uint4 o;
-            const float up = scale_f16(f, o);
-            *reinterpret_cast<uint4 *>(xq + (int64_t)t * nsl * kMoeStepK + k) = o;
-            if (lane == 0) xup[t * nsl + s] = up;
+            bf16x8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(router) + (int64_t)e * D + k)), r);
         }
+#pragma unroll
+        for (int i = 0; i < kRouteTokens; ++i) {
+            if (t0 + i >= T) break;
+            float x[8];
+            bf16x8(__ldg(reinterpret_cast<const uint4 *>(X + (int64_t)(t0 + i) * D + k)), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j & 1] = fma((double)x[j], (double)r[j], acc[i][j & 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i) {
+        if (t0 + i >= T) break;
+        double v = acc[i][0] + acc[i][1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) sums[i][warp] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < T) {
+        double v = 0.0;
+#pragma unroll
+        for (int w = 0; w < kRouteThreads / 32; ++w) v += sums[threadIdx.x][w];
+        logits[(int64_t)(t0 + threadIdx.x) * E + e] = v;
     }
 }
 
@@ -218,199 +233,168 @@ __device__ __forceinline__ float exp_f64(double d) {
     return expf(hi) * (1.0f + (float)(d - (double)hi));
 }
 
-// One warp: the k largest logits of a token (ties to the lower expert) and their weights.
-__device__ __forceinline__ void moe_choose(const MoeArgs &a, int t, int lane, float *weight, unsigned short *choice) {
-    constexpr int PER = kMoeMaxExperts / 32;
-    unsigned long long key[PER];
-    double val[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = 0ull;                                       // below every logit's key
-        val[i] = 0.0;
-        if (e < a.E) {
-            val[i] = __ldcg(a.logits + (int64_t)t * a.E + e);
-            key[i] = logit_key(val[i]);
-        }
-    }
-    double top = 0.0, sum = 0.0;
-    float mine = 0.0f;                                       // lane j: numerator of choice j
-    for (int j = 0; j < a.k; ++j) {
-        unsigned long long best = 0ull;
-        double bv = 0.0;
-        int be = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bv = val[i];
-                be = lane + 32 * i;
+constexpr int kMoeBatch = 2048;                      // (token, expert) logits that are ranked at a time
+struct MoeScratch {                                  // of the choice, before the stages are filled
+    unsigned long long key[kMoeBatch];
+    float p[kMoeBatch];                              // exp(logit - largest)
+    double top[kMoeMaxTokens];                       // largest logit
+    unsigned tokens[kMoeMaxExperts][2];              // a bit per token that chose the expert
+};
+
+// The chosen experts of every token and their weights, by the whole CTA. A thread per (token, expert) counts the token's
+// logits before its own (ties go to the lower expert), which is the expert's rank: no round waits for the one before.
+__device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeScratch &sh, float *weight, unsigned short *choice) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.E, batch = max(1, kMoeBatch / E);
+#pragma unroll 1
+    for (int t0 = 0; t0 < a.T; t0 += batch) {
+        const int nt = min(batch, a.T - t0), n = nt * E;
+        const double *logits = a.logits + (int64_t)t0 * E;
+        for (int i = threadIdx.x; i < n; i += kMoeThreads) sh.key[i] = logit_key(__ldcg(logits + i));
+        __syncthreads();
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n; i += kMoeThreads) {
+            const int t = i / E, e = i - t * E;
+            const unsigned long long *row = sh.key + t * E, mine = row[e];
+            int rank = 0;
+#pragma unroll 4
+            for (int q = 0; q < E; ++q) rank += row[q] > mine || (row[q] == mine && q < e) ? 1 : 0;
+            if (rank < a.k) {
+                choice[(t0 + t) * a.k + rank] = (unsigned short)e;
+                atomicOr(&sh.tokens[e][(t0 + t) >> 5], 1u << ((t0 + t) & 31));
             }
-        const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
-        const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32) == hi ? (unsigned)best : 0u);
-        const bool match = (unsigned)(best >> 32) == hi && (unsigned)best == lo && be != 0x7fffffff;
-        const int e = (int)__reduce_min_sync(0xffffffffu, match ? (unsigned)be : 0x7fffffffu);
-        const double v = __shfl_sync(0xffffffffu, bv, e & 31);
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i == e) key[i] = 0ull;
-        if (j == 0) {
-            top = v;
-            // the softmax's denominator
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < a.E) sum += (double)exp_f64(val[i] - top);
+            if (rank == 0) sh.top[t0 + t] = __ldcg(logits + i);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n; i += kMoeThreads) sh.p[i] = exp_f64(__ldcg(logits + i) - sh.top[t0 + i / E]);
+        __syncthreads();
+        // weights: a warp per token
+#pragma unroll 1
+        for (int t = warp; t < nt; t += kMoeWarps + kMoeHelpers) {
+            const unsigned short *mine = choice + (t0 + t) * a.k;
+            double sum = 0.0;
+            if (a.renorm) sum = lane < a.k ? (double)sh.p[t * E + mine[lane]] : 0.0;
+            else
+                for (int e = lane; e < E; e += 32) sum += (double)sh.p[t * E + e];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane < a.k) weight[(t0 + t) * a.k + lane] = (float)((double)sh.p[t * E + mine[lane]] / sum);
         }
-        const float p = exp_f64(v - top);
-        if (lane == j) mine = p;
-        if (lane == 0) choice[t * a.k + j] = (unsigned short)e;
+        __syncthreads();
     }
-    if (a.renorm) {
-        sum = lane < a.k ? (double)mine : 0.0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if (lane < a.k) weight[t * a.k + lane] = (float)((double)mine / sum);
 }
 
 // ---------------------------------------------------------------- experts
 __device__ __forceinline__ int tile_row(int g) { return 2 * (g & 3) + (g >> 2); }
-// Place of (token m, matrix row r) in a warp's sums of a tile: the 32 lanes of a store (eight rows of
-// tokens 2 t, or of tokens 2 t + 1) touch every bank once.
-__device__ __forceinline__ int sum_at(int m, int r) { return ((m ^ ((m >> 2) & 1)) << 4) + (r ^ ((m & 2) << 2)); }
-// Byte offset of float x of piece p (pieces of 128 nt floats).
-__device__ __forceinline__ uint32_t hole(int nt, int p, int x) {
-    return (uint32_t)(p * nt * 4 + (x >> 5)) * 256u + 128u + (uint32_t)(x & 31) * 4u;
+// Shared address of a warp's sum of (token m, matrix row r) of a stage's tile: the 32 lanes of a store
+// (eight rows of tokens 2 t, or of tokens 2 t + 1) touch every bank once.
+__device__ __forceinline__ uint32_t sum_at(int stage, int warp, int m, int r) {
+    const int x = ((m ^ ((m >> 2) & 1)) << 4) + (r ^ ((m & 2) << 2));
+    return kMoeTable + (uint32_t)((stage * kMoeWarps + warp) * 4 + (x >> 5)) * 256u + 128u + (uint32_t)(x & 31) * 4u;
 }
 
-// Bounded grid barrier: every CTA of the cooperative launch arrives once.
-__device__ __forceinline__ void grid_barrier(unsigned *counter, volatile int *abort) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(counter, 1u);
-        const uint64_t t0 = global_timer_ns();
-        unsigned v;
-        do {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-            if (v < gridDim.x && global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                raise_status(QLORA_ERR_TIMEOUT);
-                break;
-            }
-        } while (v < gridDim.x);
-        __threadfence();
-    }
-    __syncthreads();
-}
-
-// Everything a warp of k_moe_experts carries along.
-struct MoeWarp {
-    uint8_t *smem;
-    const MoeJob *jobs;
-    const unsigned short *order;                    // slots by job
-    int warp, lane, njobs;
-    uint32_t ring, cring, full, bar;
-    volatile int *abort;
-    // the copies' position: phase (0 gate and up, 1 down, 2 none), the group's place and how many are left
-    int iphase, igroup, iseg, ileft;                // segment iseg: job * nck + chunk
-    int issued, done, round;
-    bool dead;
-};
-
+// A phase's groups (16 warps' tiles), ordered (job, chunk, group).
 struct MoePhase {
-    int begin, end;                                 // this CTA's groups
-    int per;                                        // groups per segment (a job's chunk)
+    int job, chunk, group;                          // this CTA's first group
+    int count;                                      // its groups
+    int per, nck, nsl;                              // groups per segment (a job's chunk); chunks; slices
+    int lwk, kbs, width;                            // log2 of the warps along a row; blocks per row; outputs per expert
 };
-
-// First slice of chunk c of nck: the slices are spread evenly.
-__device__ __forceinline__ int chunk_first(int nsl, int nck, int c) {
-    const int q = nsl / nck, r = nsl % nck;
+// First slice of chunk c: the slices are spread evenly.
+__device__ __forceinline__ int chunk_first(const MoePhase &p, int c) {
+    if (p.nck == 1) return c ? p.nsl : 0;
+    const int q = p.nsl / p.nck, r = p.nsl - q * p.nck;
     return c * q + min(c, r);
 }
-// This warp's slice in a segment of a phase, or -1.
-__device__ __forceinline__ int moe_slice(const MoeArgs &a, const MoeWarp &w, int phase, int seg) {
-    if (w.dead) return -1;
-    const int nsl = phase ? a.nsl2 : a.nsl1, nck = phase ? a.nck2 : a.nck1, wk = phase ? a.wk2 : a.wk1;
-    const int c = seg % nck, first = chunk_first(nsl, nck, c), n = chunk_first(nsl, nck, c + 1) - first, kw = w.warp & (wk - 1);
-    return kw < n ? first + kw : -1;
-}
 
-// int8 constants and second-level scales of 16 rows (row(i), i = lane % 16), blocks 4 s ..: two aligned words of
-// int8 from the byte of block 4 s on, the scales of the first and the last block's groups.
-__device__ __forceinline__ void moe_scales(const int8_t *scale8, const float *scale2, uint32_t dst, int64_t row, int kbs, int s,
-                                           int lane) {
-    const int left = min(4, kbs - 4 * s);           // blocks of the step (>= 1)
-    const int64_t b = row * kbs + 4 * s;            // first block
-    const int64_t b4 = (b & ~3ll) + ((lane & 16) ? 4 : 0);
-    const int64_t n = b + left - b4;                // bytes from b4 to the end of the step's blocks
-    const uint32_t at = dst + (lane & 15) * 16 + ((lane & 16) ? 4 : 0);
-    cp4n(at, n > 0 ? scale8 + b4 : scale8, n > 4 ? 4 : n > 0 ? (int)n : 0);
-    cp4n(at + 8, scale2 + (((lane & 16) ? b + left - 1 : b) >> 8), 4);
-}
-
-// Fills the warp's next stage, if any group is left for it.
-__device__ __forceinline__ void moe_fill(const MoeArgs &a, MoeWarp &w, const MoePhase &p0, const MoePhase &p1) {
-    int sl = -1;
-    while (w.iphase < 2) {
-        if (w.ileft == 0) {                                  // the other phase
-            if (++w.iphase == 2) break;
-            w.ileft = p1.end - p1.begin;
-            w.iseg = p1.begin / p1.per;
-            w.igroup = p1.begin - w.iseg * p1.per;
-            continue;
-        }
-        sl = moe_slice(a, w, w.iphase, w.iseg);
-        if (sl >= 0) break;
-        const int skip = min(w.ileft, (w.iphase ? p1.per : p0.per) - w.igroup);   // a segment without a slice for this warp
-        w.ileft -= skip;
-        w.igroup = 0;
-        ++w.iseg;
+// Position in the CTA's groups, those of phase 0 and then those of phase 1, with what its segment (job and chunk) fixes.
+struct MoeCursor {
+    int phase, jobno, chunk, group, left, run;      // run: groups left in the segment
+    int first, slices, row, step;                   // the chunk's slices; the group's first weight row; rows of a group
+    MoeJob job;
+    __device__ __forceinline__ void segment(const MoePhase &p, const MoeJob *jobs) {
+        run = min(left, p.per - group);
+        if (run <= 0) return;
+        first = chunk_first(p, chunk);
+        slices = chunk_first(p, chunk + 1) - first;
+        job = jobs[jobno];
+        step = (phase ? 16 : 8) << (4 - p.lwk);
+        row = job.expert * p.width + group * step;
     }
-    if (w.iphase < 2) {
-        const int st = w.issued & (kMoeStages - 1), lane = w.lane;
-        const uint32_t dst = w.ring + st * kMoeStageBytes, cdst = w.cring + st * kMoeScaleBytes, bar = w.full + 8 * st;
-        if (w.iphase == 0) {
-            const int tile = (w.igroup * kMoeWarps + w.warp) / a.wk1, f0 = min(tile * 8, a.F - 8);
-            const int row = w.jobs[w.iseg / a.nck1].expert * a.F + f0;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kMoeStageBytes);
-                tma_load_2d(dst, &a.gate.codes, bar, sl * 128, row);
-                tma_load_2d(dst + 1024, &a.up.codes, bar, sl * 128, row);
-            }
-            moe_scales((lane & 8) ? a.up.scale8 : a.gate.scale8, (lane & 8) ? a.up.scale2 : a.gate.scale2, cdst, row + (lane & 7),
-                       a.D / 64, sl, lane);
-        } else {
-            const int tile = (w.igroup * kMoeWarps + w.warp) / a.wk2, d0 = min(tile * 16, a.D - 16);
-            const int row = w.jobs[w.iseg / a.nck2].expert * a.D + d0;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kMoeStageBytes);
-                tma_load_2d(dst, &a.down.codes, bar, sl * 128, row);
-            }
-            moe_scales(a.down.scale8, a.down.scale2, cdst, row + (lane & 15), a.F / 64, sl, lane);
-        }
-        ++w.issued;
-        --w.ileft;
-        if (++w.igroup == (w.iphase ? p1.per : p0.per)) {
-            w.igroup = 0;
-            ++w.iseg;
-        }
+    __device__ __forceinline__ void enter(int ph, const MoePhase &p, const MoeJob *jobs) {
+        phase = ph;
+        jobno = p.job;
+        chunk = p.chunk;
+        group = p.group;
+        left = p.count;
+        segment(p, jobs);
     }
-    cp_commit();
+    __device__ __forceinline__ void start(const MoePhase &p0, const MoePhase &p1, const MoeJob *jobs) {
+        enter(0, p0, jobs);
+        if (left == 0) enter(1, p1, jobs);
+    }
+    __device__ __forceinline__ void next(const MoePhase &p0, const MoePhase &p1, const MoeJob *jobs) {
+        --left;
+        ++group;
+        row += step;
+        if (--run > 0) return;
+        if (left == 0) {
+            if (phase == 0) enter(1, p1, jobs);
+            return;
+        }
+        const MoePhase &p = phase ? p1 : p0;
+        group = 0;
+        if (++chunk == p.nck) {
+            chunk = 0;
+            ++jobno;
+        }
+        segment(p, jobs);
+    }
+};
+
+// This CTA's groups of a phase, an even share.
+__device__ __forceinline__ MoePhase moe_share(int njobs, int nck, int nsl, int lwk, int width, int rows, int cols) {
+    MoePhase p;
+    const int tg = kMoeWarps >> lwk;
+    p.per = (width / rows + tg - 1) >> (4 - lwk);
+    const unsigned n = (unsigned)njobs * nck * p.per, nc = gridDim.x, c = blockIdx.x, q = n / nc, r = n - q * nc;
+    const unsigned begin = c * q + min(c, r), seg = begin / p.per;
+    p.count = (int)(q + (c < r ? 1 : 0));
+    p.group = (int)(begin - seg * p.per);
+    p.job = nck == 1 ? (int)seg : (int)(seg / nck);
+    p.chunk = (int)seg - p.job * nck;
+    p.nck = nck;
+    p.nsl = nsl;
+    p.lwk = lwk;
+    p.kbs = cols / 64;
+    p.width = width;
+    return p;
 }
 
-__device__ __noinline__ void moe_drain(uint32_t full, int done, int issued) {
-    cp_wait<0>();
+struct MoeCta {
+    uint8_t *window;                                // the shared window's address 0
+    const MoeJob *jobs;
+    const unsigned short *order;                    // slots by job
+    uint32_t full, done, go;                        // barriers: per stage; per stage; the first grid barrier is passed
+    volatile int *abort;
+};
+
+// Bounded grid barrier for one thread of the CTA, after the CTA's writes are ordered before it.
+__device__ __forceinline__ void grid_arrive_wait(unsigned *counter, volatile int *abort) {
+    __threadfence();
+    atomicAdd(counter, 1u);
     const uint64_t t0 = global_timer_ns();
-    for (; done < issued; ++done)
-        while (!mbar_try_wait(full + 8 * (done & (kMoeStages - 1)), (done / kMoeStages) & 1))
-            if (global_timer_ns() - t0 > kWaitLimitNs) return;
-}
-
-__device__ __forceinline__ float i8_f32(uint32_t word, int i) {     // byte i of word ^ 0x80808080, as int8
-    return __uint_as_float(prmt(word, 0x4b000000u, 0x7440u + i)) - 8388736.0f;
+    while (true) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        if (v >= gridDim.x) break;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            raise_status(QLORA_ERR_TIMEOUT);
+            break;
+        }
+    }
+    __threadfence();
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -436,300 +420,434 @@ __device__ __forceinline__ void moe_hidden(const MoeArgs &a, int slot, int k, fl
     for (int i = 0; i < 8; ++i) f[i] = silu(f[i]) * u[i];
 }
 
-// Runs groups g0 .. g1 - 1 of segment `seg` of a phase: tokens of the job (up to 8 NT) into registers, then rounds of
-// R tiles per warp, summed over the warps: h, or the partial sums of the outputs.
-template <int NT, int PHASE>
-__device__ __forceinline__ void moe_run(const MoeArgs &a, MoeWarp &w, const MoePhase &p0, const MoePhase &p1, int seg, int g0, int g1) {
-    constexpr int R = NT == 1 ? 2 : 1;
-    const int lane = w.lane, g = lane >> 2, t = lane & 3;
-    const int wk = PHASE ? a.wk2 : a.wk1, tg = kMoeWarps / wk, kw = w.warp % wk, tw = w.warp / wk;
-    const int kbs = (PHASE ? a.F : a.D) / 64;
-    const int nck = PHASE ? a.nck2 : a.nck1, nsl = PHASE ? a.nsl2 : a.nsl1, chunk = seg % nck;
-    const MoeJob job = w.jobs[seg / nck];
-    const int mn = job.count, sl = moe_slice(a, w, PHASE, seg);
-    const int act = chunk_first(nsl, nck, chunk + 1) - chunk_first(nsl, nck, chunk);   // warps with a slice
-    const int piece0 = tw * R * wk + kw;
-    constexpr int kBufPieces = kMoeWarps * R;
-
-    uint32_t xb[NT][32];
-    float up[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        up[nt][0] = up[nt][1] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) xb[nt][i] = 0u;
-    }
-    if (sl >= 0) {
-        if (PHASE == 0) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int m = 8 * nt + g;
-                if (m < mn) {
-                    const int tok = w.order[job.first + m] / a.k;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.xq + ((int64_t)tok * a.nsl1 + sl) * kMoeStepK) + 2 * t;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 v = __ldcg(src + 8 * (i >> 1) + (i & 1));
-                        xb[nt][4 * i] = v.x;
-                        xb[nt][4 * i + 1] = v.y;
-                        xb[nt][4 * i + 2] = v.z;
-                        xb[nt][4 * i + 3] = v.w;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (8 * nt + 2 * t + i < mn)
-                        up[nt][i] = __ldcg(a.xup + (w.order[job.first + 8 * nt + 2 * t + i] / a.k) * a.nsl1 + sl);
-            }
-        } else {
-            // h is converted here, four tokens at a time through the places of this warp's own sums
-            auto stage = [&](int m, int u) {
-                const int p = (m >> 1) * kBufPieces + (NT == 1 ? (m & 1) * wk : 0);
-                return reinterpret_cast<uint4 *>(w.smem + hole(NT, p + piece0, 4 * u + (NT == 1 ? 0 : (m & 1) * 128)));
-            };
-            const int k = sl * kMoeStepK + 8 * lane;
-#pragma unroll
-            for (int q = 0; q < 2 * NT; ++q) {
-                if (4 * q >= mn) break;
-                float f[4][8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-                    if (4 * q + i < mn && k < a.F) moe_hidden(a, w.order[job.first + 4 * q + i], k, f[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (4 * q + i >= mn) break;
-                    uint4 o;
-                    const float s = scale_f16(f[i], o);
-                    *stage(i, lane) = o;
-                    const int m = (4 * q + i) & 7;
-                    up[q / 2][0] = 2 * t == m ? s : up[q / 2][0];
-                    up[q / 2][1] = 2 * t + 1 == m ? s : up[q / 2][1];
-                }
-                __syncwarp();
-                if ((g >> 2) == (q & 1) && 8 * (q / 2) + g < mn) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 v = *stage(g & 3, 8 * (i >> 1) + 2 * t + (i & 1));
-                        xb[q / 2][4 * i] = v.x;
-                        xb[q / 2][4 * i + 1] = v.y;
-                        xb[q / 2][4 * i + 2] = v.z;
-                        xb[q / 2][4 * i + 3] = v.w;
-                    }
-                }
-                __syncwarp();
-            }
-        }
-    }
-
-    // this lane's codes in a stage (matrix rows g, g + 8: stage rows tile_row(g), + 8), constants, places of its sums
-    const uint8_t *at[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        at[b] = w.smem + kMoeRingAt + w.warp * (kMoeStages * kMoeStageBytes) + tile_row(g) * 128 +
-                (((2 * b + (t >> 1)) ^ tile_row(g)) << 4) + (t & 1) * 8;
-    const uint8_t *sc = w.smem + kMoeScaleAt + w.warp * (kMoeStages * kMoeScaleBytes) + tile_row(g) * 16;
-    int put[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) put[e] = (int)hole(NT, 0, sum_at(2 * t + (e & 1), g + 8 * (e >> 1)));
-    const float mu0 = __ldg(PHASE ? a.down.offset : a.gate.offset), mu1 = __ldg(PHASE ? a.down.offset : a.up.offset);
-    // a tile's rows start at a multiple of 8, so the byte of the first block in its word depends on the row alone
-    const int shift = 8 * ((tile_row(g) * kbs) & 3);
-    const uint32_t lane4 = lane * 4;
-
-    auto add_round = [&](int round, int i0, int rn) {
-        if (!moe_wait(w.bar, round & 1, w.abort)) return;
-        constexpr int ROWS = PHASE ? 16 : 8;                 // outputs of a tile
-        for (int e = w.warp * 32 + lane; e < tg * R * ROWS * 8 * NT; e += kMoeThreads) {
-            const int r = e & (ROWS - 1), m = (e / ROWS) & (8 * NT - 1), ti = e / (ROWS * 8 * NT), i = ti & (R - 1);
-            const int tile = (i0 + i) * tg + ti / R;
-            if (i >= rn || m >= mn || tile * ROWS >= (PHASE ? a.D : a.F)) continue;
-            const uint8_t *src = w.smem + hole(NT, (round & 1) * kBufPieces + ti * wk, sum_at(m, r));
-            float y = 0.0f;
-#pragma unroll 8
-            for (int q = 0; q < act; ++q) y += *reinterpret_cast<const float *>(src + q * (NT * 1024));
-            const int slot = w.order[job.first + m], out = tile * ROWS + (r & 8) + tile_row(r & 7);
-            if (PHASE == 0) {
-                const uint8_t *src1 = w.smem + hole(NT, (round & 1) * kBufPieces + ti * wk, sum_at(m, r + 8));
-                float u = 0.0f;
-#pragma unroll 8
-                for (int q = 0; q < act; ++q) u += *reinterpret_cast<const float *>(src1 + q * (NT * 1024));
-                if (a.nck1 == 1) {
-                    __stcg(a.h + (int64_t)slot * a.F + out, silu(y) * u);
-                } else {
-                    float *dst = a.h + ((int64_t)slot * a.nck1 + chunk) * 2 * a.F + out;
-                    __stcg(dst, y);
-                    __stcg(dst + a.F, u);
-                }
-            } else {
-                __stcg(a.part + ((int64_t)slot * a.nck2 + chunk) * a.D + out, y);
-            }
-        }
-    };
-
-    for (int i0 = g0; i0 < g1; i0 += R, ++w.round) {
-        const int rn = min(R, g1 - i0);
-        if (sl < 0 && i0 > g0) add_round(w.round - 1, i0 - R, R);
-        int used = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (sl < 0 || w.dead || i >= rn) break;
-            const int st = w.done & (kMoeStages - 1), so = st * kMoeStageBytes;
-            if (i == 0) cp_wait<kMoeStages - 1>();
-            else cp_wait<kMoeStages - 2>();
-            if (!moe_wait(w.full + 8 * st, (w.done / kMoeStages) & 1, w.abort)) {
-                moe_drain(w.full, w.done, w.issued);         // the CTA goes on without this warp's slices
-                w.dead = true;
-                break;
-            }
-            __syncwarp();                                    // every lane's copies of the constants have landed
-            ++w.done;
-            ++used;
-            // c = scale8 (scale2 / 127) + offset of the four blocks of both rows
-            float c0[4], c1[4];
-            {
-                const uint4 q0 = *reinterpret_cast<const uint4 *>(sc + st * kMoeScaleBytes);
-                const uint4 q1 = *reinterpret_cast<const uint4 *>(sc + st * kMoeScaleBytes + 128);
-                const uint32_t w0 = __funnelshift_r(q0.x, q0.y, shift) ^ 0x80808080u;
-                const uint32_t w1 = __funnelshift_r(q1.x, q1.y, shift) ^ 0x80808080u;
-                const float s0 = __uint_as_float(q0.z) * (1.0f / 127.0f), s1 = __uint_as_float(q1.z) * (1.0f / 127.0f);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    c0[b] = fmaf(i8_f32(w0, b), s0, mu0);
-                    c1[b] = fmaf(i8_f32(w1, b), s1, mu1);
-                }
-                if (kbs & 3) {                               // a second-level group may end inside the step
-                    const int tile = (i0 + i) * tg + tw;
-                    const int row = PHASE ? job.expert * a.D + min(tile * 16, a.D - 16) : job.expert * a.F + min(tile * 8, a.F - 8);
-                    const int64_t b0 = (int64_t)(row + tile_row(g)) * kbs + 4 * sl, b1 = PHASE ? b0 + 8 * kbs : b0;
-                    const float z0 = __uint_as_float(q0.w) * (1.0f / 127.0f), z1 = __uint_as_float(q1.w) * (1.0f / 127.0f);
-#pragma unroll
-                    for (int b = 1; b < 4; ++b) {
-                        if (((b0 + b) >> 8) != (b0 >> 8)) c0[b] = fmaf(i8_f32(w0, b), z0, mu0);
-                        if (((b1 + b) >> 8) != (b1 >> 8)) c1[b] = fmaf(i8_f32(w1, b), z1, mu1);
-                    }
-                }
-            }
-            float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(at[b] + so), v = *reinterpret_cast<const uint2 *>(at[b] + so + 1024);
-                float cc[NT][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t wu = j ? u.y : u.x, wv = j ? v.y : v.x;
-                    uint32_t p[4], q[4];
-#pragma unroll
-                    for (int i2 = 0; i2 < 4; ++i2) {
-                        p[i2] = *reinterpret_cast<const uint32_t *>(w.smem + prmt(wu, lane4, 0x5504u | ((uint32_t)i2 << 4)));
-                        q[i2] = *reinterpret_cast<const uint32_t *>(w.smem + prmt(wv, lane4, 0x5504u | ((uint32_t)i2 << 4)));
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t *x = xb[nt] + 8 * b + 4 * j;
-                        if (j == 0) mma_f16_first(cc[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
-                        else mma_f16(cc[nt], p[0], q[0], p[1], q[1], x[0], x[1]);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t *x = xb[nt] + 8 * b + 4 * j;
-                        mma_f16(cc[nt], p[2], q[2], p[3], q[3], x[2], x[3]);
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    acc[nt][0] = fmaf(c0[b], cc[nt][0], acc[nt][0]);
-                    acc[nt][1] = fmaf(c0[b], cc[nt][1], acc[nt][1]);
-                    acc[nt][2] = fmaf(c1[b], cc[nt][2], acc[nt][2]);
-                    acc[nt][3] = fmaf(c1[b], cc[nt][3], acc[nt][3]);
-                }
-            }
-            // the round before, whose buffer the next round needs: a step after it ended
-            if (i == 0 && i0 > g0) add_round(w.round - 1, i0 - R, R);
-            uint8_t *piece = w.smem + ((w.round & 1) * kBufPieces + piece0 + i * wk) * (NT * 1024);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (8 * nt + 2 * t + (e & 1) < mn)
-                        *reinterpret_cast<float *>(piece + nt * 1024 + put[e]) = acc[nt][e] * up[nt][e & 1];
-        }
-        __syncwarp();                                        // the stages have been read, the sums written
-        if (lane == 0) mbar_arrive(w.bar);
-        for (int i = 0; i < used; ++i) moe_fill(a, w, p0, p1);
-    }
-    const int last = g0 + (g1 - g0 - 1) / R * R;
-    add_round(w.round - 1, last, g1 - last);
-    __syncthreads();                                         // the sums' places are free for the next run
+// A word of the lookup table, which no one writes after it was filled: the load may move freely.
+__device__ __forceinline__ uint32_t table_word(uint32_t at) {
+    uint32_t v;
+    asm("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
 }
 
-template <int PHASE>
-__device__ __forceinline__ void moe_phase(const MoeArgs &a, MoeWarp &w, const MoePhase &p0, const MoePhase &p1) {
-    const MoePhase &p = PHASE ? p1 : p0;
-    for (int i = p.begin; i < p.end;) {
-        const int seg = i / p.per, first = seg * p.per, n = min(p.end, first + p.per);
-        if (w.jobs[seg / (PHASE ? a.nck2 : a.nck1)].count <= 8) moe_run<1, PHASE>(a, w, p0, p1, seg, i - first, n - first);
-        else moe_run<2, PHASE>(a, w, p0, p1, seg, i - first, n - first);
-        i = n;
+// ---------------- the sixteen warps that multiply
+// Token operands of a slice: lane (g, t) holds token g of the job, inputs 64 b + 16 t + 8 j + 0..7 in
+// xb[8 b + 4 j ..]; up: 2^e of tokens 2 t and 2 t + 1.
+__device__ __forceinline__ void moe_tokens(const MoeArgs &a, const MoeCta &c, int phase, const MoeJob &job, int sl,
+                                           uint32_t (&xb)[32], float (&up)[2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    up[0] = up[1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) xb[i] = 0u;
+    if (phase == 0) {
+        const int s0 = c.order[job.first + min(2 * t, job.count - 1)], s1 = c.order[job.first + min(2 * t + 1, job.count - 1)];
+        if (g < job.count) {
+            const int tok = c.order[job.first + g] / a.k;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.xq + ((int64_t)tok * a.nsl1 + sl) * kMoeStepK) + 2 * t;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = __ldcg(src + 8 * (i >> 1) + (i & 1));
+                xb[4 * i] = v.x;
+                xb[4 * i + 1] = v.y;
+                xb[4 * i + 2] = v.z;
+                xb[4 * i + 3] = v.w;
+            }
+        }
+        up[0] = __ldcg(a.xup + (s0 / a.k) * a.nsl1 + sl);
+        up[1] = __ldcg(a.xup + (s1 / a.k) * a.nsl1 + sl);
+    } else {
+        // lane u converts inputs 8 u .. 8 u + 7 of a token's hidden values; the token's four lanes collect theirs
+        const int k = sl * kMoeStepK + 8 * lane;
+#pragma unroll 1
+        for (int m = 0; m < job.count; ++m) {
+            float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+            if (k < a.F) moe_hidden(a, c.order[job.first + m], k, f);
+            uint4 o;
+            const float s = scale_f16(f, o);
+            up[0] = 2 * t == m ? s : up[0];
+            up[1] = 2 * t + 1 == m ? s : up[1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int src = 8 * (i >> 1) + 2 * t + (i & 1);
+                const uint32_t v0 = __shfl_sync(0xffffffffu, o.x, src), v1 = __shfl_sync(0xffffffffu, o.y, src);
+                const uint32_t v2 = __shfl_sync(0xffffffffu, o.z, src), v3 = __shfl_sync(0xffffffffu, o.w, src);
+                xb[4 * i] = g == m ? v0 : xb[4 * i];
+                xb[4 * i + 1] = g == m ? v1 : xb[4 * i + 1];
+                xb[4 * i + 2] = g == m ? v2 : xb[4 * i + 2];
+                xb[4 * i + 3] = g == m ? v3 : xb[4 * i + 3];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // this lane's codes of block b (matrix rows g, g + 8: rows tile_row(g), + 8 of the warp's 16), constants, sums
+    int at[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) at[b] = tile_row(g) * 128 + (((2 * b + (t >> 1)) ^ tile_row(g)) << 4) + (t & 1) * 8;
+    const uint8_t *sc = c.window + kMoeScaleAt + tile_row(g) * kMoeScaleRow + warp * 16;
+    uint8_t *put[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put[e] = c.window + sum_at(0, warp, 2 * t + (e & 1), g + 8 * (e >> 1));
+    const uint32_t table = kMoeTable | (uint32_t)(lane * 4);
+
+    uint32_t xb[32];
+    float up[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) xb[i] = 0u;
+    int n = 0;                                               // group of the CTA
+#pragma unroll 1
+    for (int phase = 0; phase < 2; ++phase) {
+        const MoePhase &p = phase ? p1 : p0;
+        if (phase == 1 && p.count > 0 && !moe_wait(c.go, 0, c.abort)) return;   // every CTA's hidden values
+        int jobno = p.job, chunk = p.chunk, run = min(p.count, p.per - p.group);
+#pragma unroll 1
+        for (int left = p.count; left > 0; left -= run, run = min(left, p.per)) {
+            const int first = chunk_first(p, chunk), kw = warp & ((1 << p.lwk) - 1);
+            const MoeJob job = c.jobs[jobno];
+            const bool mine = kw < chunk_first(p, chunk + 1) - first;     // the warp has a slice in this segment
+            const int mn = job.count;
+            if (mine) moe_tokens(a, c, phase, job, first + kw, xb, up);
+            // phase 0: all warps' eight gate rows, then all warps' up rows; phase 1: 16 rows per warp
+            const int lo_at = warp * (phase ? 2048 : 1024), hi_at = phase ? 1024 : kMoeWarps * 1024;
+#pragma unroll 1
+            for (const int end = n + run; n < end; ++n) {
+                const int st = n & (kMoeStages - 1);
+                if (!moe_wait(c.full + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
+                if (mine) {
+                    const uint8_t *lo = c.window + stage_at(st) + lo_at, *hi = lo + hi_at;
+                    const float4 f0 = *reinterpret_cast<const float4 *>(sc + st * kMoeScaleBytes);
+                    const float4 f1 = *reinterpret_cast<const float4 *>(sc + st * kMoeScaleBytes + 8 * kMoeScaleRow);
+                    const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(lo + at[b]), v = *reinterpret_cast<const uint2 *>(hi + at[b]);
+                        float cc[4];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t wu = j ? u.y : u.x, wv = j ? v.y : v.x;
+                            uint32_t d[4], e[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                d[i] = table_word(prmt(wu, table, 0x7604u | ((uint32_t)i << 4)));
+                                e[i] = table_word(prmt(wv, table, 0x7604u | ((uint32_t)i << 4)));
+                            }
+                            const uint32_t *x = xb + 8 * b + 4 * j;
+                            if (j == 0) mma_f16_first(cc, d[0], e[0], d[1], e[1], x[0], x[1]);
+                            else mma_f16(cc, d[0], e[0], d[1], e[1], x[0], x[1]);
+                            mma_f16(cc, d[2], e[2], d[3], e[3], x[2], x[3]);
+                        }
+                        acc[0] = fmaf(c0[b], cc[0], acc[0]);
+                        acc[1] = fmaf(c0[b], cc[1], acc[1]);
+                        acc[2] = fmaf(c1[b], cc[2], acc[2]);
+                        acc[3] = fmaf(c1[b], cc[3], acc[3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (2 * t + (e & 1) < mn)
+                            *reinterpret_cast<float *>(put[e] + st * (kMoeWarps * 1024)) = acc[e] * up[e & 1];
+                }
+                __syncwarp();                                // the stage has been read, the sums written
+                if (lane == 0) mbar_arrive(c.done + 8 * st);
+            }
+            if (++chunk == p.nck) {
+                chunk = 0;
+                ++jobno;
+            }
+        }
+    }
+}
+
+// ---------------- the seven warps around them
+// Copies of one group's codes. Rows past an expert's last tile are the next expert's or zeros (a group's tiles need not
+// divide the expert): their sums are not used.
+__device__ __forceinline__ void moe_copy(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur, int st) {
+    const int lane = threadIdx.x & 31, n = cur.slices, rows = cur.phase ? 16 : 8, tg = kMoeWarps >> p.lwk;
+    const uint32_t bar = c.full + 8 * st, base = stage_at(st);
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * tg * 2048);
+    __syncwarp();
+    if (cur.phase ? a.whole2 : a.whole1) {
+        // one copy per tile and weight
+        if (lane < tg) {
+            const bool less = n * p.nck < p.nsl;             // a chunk one slice shorter than the longest
+            const uint32_t dst = base + (lane << p.lwk) * rows * 128;
+            const int row = cur.row + lane * rows;
+            if (cur.phase) {
+                tma_load_3d(dst, less ? &a.down.codes_less : &a.down.codes, bar, 0, row, cur.first);
+            } else {
+                tma_load_3d(dst, less ? &a.gate.codes_less : &a.gate.codes, bar, 0, row, cur.first);
+                tma_load_3d(dst + kMoeWarps * 1024, less ? &a.up.codes_less : &a.up.codes, bar, 0, row, cur.first);
+            }
+        }
+    } else {
+        const int side = lane >> p.lwk, s = lane & ((1 << p.lwk) - 1);
+        if (lane < kMoeWarps && s < n) {
+            const uint32_t dst = base + lane * rows * 128;
+            const int row = cur.row + side * rows, x = (cur.first + s) * 128;
+            if (cur.phase) {
+                tma_load_2d(dst, &a.down.codes, bar, x, row);
+            } else {
+                tma_load_2d(dst, &a.gate.codes, bar, x, row);
+                tma_load_2d(dst + kMoeWarps * 1024, &a.up.codes, bar, x, row);
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// Constants of a group. A unit is four blocks of a row: (tile of the group, row, slice), slices fastest, so that the
+// lanes of a warp read runs of a row; at most 256 units for the lanes of four warps. A unit's place relative to the
+// group's first row is the same in every group of a chunk.
+constexpr int kMoeUnits = (256 + 32 * kMoeScalers - 1) / (32 * kMoeScalers);   // per lane
+struct MoeUnits {
+    int off[kMoeUnits];                                      // first block, relative to the group's first row; -1: none
+    int dst[kMoeUnits];                                      // shared offset in a stage
+    int valid[kMoeUnits];                                    // blocks of the unit that the row has (up to 4)
+    int up, key;                                             // bit i: unit i is a row of the up weight; phase and chunk
+};
+struct MoeRaw {
+    uint32_t w[kMoeUnits][2];                                // the aligned words of int8 that hold a unit's blocks
+    float s[kMoeUnits][2];                                   // second-level scales of the unit's first and last block
+    int low;                                                 // the group's first block, low bits
+};
+
+__device__ __forceinline__ void moe_units(const MoePhase &p, const MoeCursor &cur, MoeUnits &u) {
+    const int first = cur.first, n = cur.slices, phase = cur.phase, rows = phase ? 16 : 8;
+    const int hl = threadIdx.x - 32 * (kMoeWarps + 1 + kMoeAdders), units = (16 * n) << (4 - p.lwk);
+    u.up = 0;
+#pragma unroll
+    for (int i = 0; i < kMoeUnits; ++i) {
+        const int q = hl + 32 * kMoeScalers * i, rs = q / n, s = q - rs * n, r = rs & 15, side = rs >> 4;
+        u.off[i] = q < units ? (side * rows + (phase ? r : r & 7)) * p.kbs + 4 * (first + s) : -1;
+        u.dst[i] = r * kMoeScaleRow + ((side << p.lwk) + s) * 16;
+        u.up |= (phase == 0 && r >= 8 ? 1 : 0) << i;
+        u.valid[i] = min(4, p.kbs - 4 * (first + s));
+    }
+    u.key = phase * 65536 + cur.chunk;
+}
+
+// Loads the units of a group (rows past the expert's outputs stay zero: their sums are not used). ALIGNED: rows of a
+// multiple of four blocks, so that a unit is one word, of one second-level group.
+template <bool ALIGNED>
+__device__ __forceinline__ void moe_raw(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur,
+                                        const MoeUnits &u, MoeRaw &raw) {
+    const int64_t base = (int64_t)cur.row * p.kbs;
+    const int room = (p.width - cur.group * cur.step) * p.kbs;   // blocks to the expert's end
+    raw.low = (int)(base & 255);
+    const MoeWeight &first = cur.phase ? a.down : a.gate;
+    const int8_t *s8[2] = {first.scale8 + (base - (base & 3)), cur.phase ? nullptr : a.up.scale8 + (base - (base & 3))};
+    const float *s2[2] = {first.scale2 + (base >> 8), cur.phase ? nullptr : a.up.scale2 + (base >> 8)};
+#pragma unroll
+    for (int i = 0; i < kMoeUnits; ++i) {
+        raw.w[i][0] = raw.w[i][1] = 0u;
+        raw.s[i][0] = raw.s[i][1] = 0.0f;
+        if ((unsigned)u.off[i] < (unsigned)room) {
+            const bool up = (u.up >> i) & 1;
+            const int8_t *p8 = up ? s8[1] : s8[0];
+            const float *p2 = up ? s2[1] : s2[0];
+            const int b = raw.low + u.off[i], last = b + u.valid[i] - 1;         // first and last block, from base - low on
+            raw.w[i][0] = __ldg(reinterpret_cast<const unsigned int *>(p8 + (((raw.low & 3) + u.off[i]) & ~3)));
+            raw.s[i][0] = __ldg(p2 + (b >> 8));
+            if (!ALIGNED) {
+                raw.w[i][1] = __ldg(reinterpret_cast<const unsigned int *>(p8 + (((raw.low & 3) + u.off[i] + u.valid[i] - 1) & ~3)));
+                raw.s[i][1] = __ldg(p2 + (last >> 8));
+            }
+        }
+    }
+}
+
+template <bool ALIGNED>
+__device__ __forceinline__ void moe_constants(const MoeCta &c, int st, const MoeUnits &u, const MoeRaw &raw, float mu0, float mu1) {
+#pragma unroll
+    for (int i = 0; i < kMoeUnits; ++i) {
+        if (u.off[i] < 0) continue;
+        const int b0 = raw.low + u.off[i];                   // first block, modulo 256 and modulo 4
+        const uint32_t w = ALIGNED ? raw.w[i][0] : __funnelshift_r(raw.w[i][0], raw.w[i][1], 8 * (b0 & 3));
+        const float mu = (u.up >> i) & 1 ? mu1 : mu0, s0 = raw.s[i][0] * (1.0f / 127.0f);
+        float v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float s = s0;
+            if (!ALIGNED && b >= 256 - (b0 & 255)) s = raw.s[i][1] * (1.0f / 127.0f);   // the next second-level group
+            v[b] = fmaf((float)(int8_t)(w >> (8 * b)), s, mu);
+            if (!ALIGNED && b >= u.valid[i]) v[b] = 0.0f;
+        }
+        *reinterpret_cast<float4 *>(c.window + kMoeScaleAt + st * kMoeScaleBytes + u.dst[i]) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// A token's value of one output: the warps' sums, in a fixed order.
+__device__ __forceinline__ float moe_sum(const uint8_t *src, int act) {
+    if (act == kMoeWarps) {
+        float v[kMoeWarps];
+#pragma unroll
+        for (int q = 0; q < kMoeWarps; ++q) v[q] = *reinterpret_cast<const float *>(src + q * 1024);
+#pragma unroll
+        for (int o = 1; o < kMoeWarps; o *= 2)
+#pragma unroll
+            for (int q = 0; q < kMoeWarps; q += 2 * o) v[q] += v[q + o];
+        return v[0];
+    }
+    float y = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < act; ++q) y += *reinterpret_cast<const float *>(src + q * 1024);
+    return y;
+}
+
+// The sums of one group: hidden values, or partial sums of outputs.
+__device__ __forceinline__ void moe_sums(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur, int st) {
+    const int lane = threadIdx.x & 31, act = cur.slices, ltg = 4 - p.lwk, log = cur.phase ? 4 : 3;
+    const int total = cur.job.count << (log + ltg), out0 = cur.group * cur.step;
+    // element: row of the tile, tile of the group, token. In phase 0 lanes 0..15 add gate products, lanes 16..31 the up
+    // products of the same outputs.
+    const int half = cur.phase ? 0 : lane >> 4, width = cur.phase ? 32 : 16;
+#pragma unroll 1
+    for (int e0 = 0; e0 < total; e0 += width) {
+        const int e = e0 + (lane & (width - 1));
+        const int r = e & ((1 << log) - 1), side = (e >> log) & ((1 << ltg) - 1), m = min(e >> (log + ltg), kMoeJob - 1);
+        const int out = out0 + (side << log) + (r & 8) + tile_row(r & 7);
+        const float y = moe_sum(c.window + sum_at(st, side << p.lwk, m, r + 8 * half), act);
+        const float u = cur.phase ? 0.0f : __shfl_xor_sync(0xffffffffu, y, 16);
+        if (half || e >= total || out >= p.width) continue;
+        const int slot = c.order[cur.job.first + m];
+        if (cur.phase) {
+            __stcg(a.part + ((int64_t)slot * a.nck2 + cur.chunk) * a.D + out, y);
+        } else if (a.nck1 == 1) {
+            __stcg(a.h + (int64_t)slot * a.F + out, silu(y) * u);
+        } else {
+            float *dst = a.h + ((int64_t)slot * a.nck1 + cur.chunk) * 2 * a.F + out;
+            __stcg(dst, y);
+            __stcg(dst + a.F, u);
+        }
+    }
+}
+
+// Group n + 4 follows in the stage of group n once that is done: copied by one warp, its constants made by four; the
+// sums of group n, whose places group n + 4 takes, by one of two warps in turn.
+__device__ __forceinline__ void moe_copier(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
+    const int total = p0.count + p1.count;
+    MoeCursor cur;
+    cur.start(p0, p1, c.jobs);
+#pragma unroll 1
+    for (int n = 0; n < total; ++n) {
+        const int st = n & (kMoeStages - 1);
+        if (n >= kMoeStages && !moe_wait(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return;
+        moe_copy(a, c, cur.phase ? p1 : p0, cur, st);
+        cur.next(p0, p1, c.jobs);
+    }
+}
+
+__device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
+    const int lane = threadIdx.x & 31, h = (threadIdx.x >> 5) - kMoeWarps - 1, total = p0.count + p1.count;
+    // every CTA's hidden values: this CTA's are written once both warps are past its last group of phase 0
+    auto meet = [&]() {
+        named_bar_sync(1, 32 * kMoeAdders);
+        if (h == 0 && lane == 0) {
+            grid_arrive_wait(a.counters, c.abort);
+            mbar_arrive(c.go);
+        }
+        __syncwarp();
+    };
+    if (lane < kMoeStages && (lane & (kMoeAdders - 1)) == h) mbar_arrive(c.full + 8 * lane);   // no sums before the first use
+    __syncwarp();
+    if (p0.count == 0) meet();
+    MoeCursor cur;
+    cur.start(p0, p1, c.jobs);
+#pragma unroll 1
+    for (int n = 0; n < total; ++n) {
+        const int st = n & (kMoeStages - 1);
+        if ((n & (kMoeAdders - 1)) == h) {
+            if (!moe_wait(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
+            moe_sums(a, c, cur.phase ? p1 : p0, cur, st);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.full + 8 * st);
+        }
+        cur.next(p0, p1, c.jobs);
+        if (n == p0.count - 1) meet();
+    }
+}
+
+__device__ __forceinline__ void moe_scaler(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
+    const int lane = threadIdx.x & 31, total = p0.count + p1.count;
+    const float mu[3] = {__ldg(a.gate.offset), __ldg(a.up.offset), __ldg(a.down.offset)};
+    // two groups' constants are loaded ahead, in registers
+    MoeUnits ua, ub;
+    MoeRaw ra, rb;
+    MoeCursor ahead;
+    ahead.start(p0, p1, c.jobs);
+    ua.key = ub.key = -1;
+    auto load = [&](MoeUnits &u, MoeRaw &r) {
+        const MoePhase &p = ahead.phase ? p1 : p0;
+        if (u.key != ahead.phase * 65536 + ahead.chunk) moe_units(p, ahead, u);
+        if (p.kbs & 3) moe_raw<false>(a, c, p, ahead, u, r);
+        else moe_raw<true>(a, c, p, ahead, u, r);
+        ahead.next(p0, p1, c.jobs);
+    };
+    auto step = [&](int n, MoeUnits &u, MoeRaw &r) {
+        const int st = n & (kMoeStages - 1), phase = n >= p0.count;
+        if (n >= kMoeStages && !moe_wait(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return false;
+        const float mu0 = phase ? mu[2] : mu[0];
+        if ((phase ? p1 : p0).kbs & 3) moe_constants<false>(c, st, u, r, mu0, mu[1]);
+        else moe_constants<true>(c, st, u, r, mu0, mu[1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.full + 8 * st);
+        if (n + 2 < total) load(u, r);
+        return true;
+    };
+    if (total > 0) load(ua, ra);
+    if (total > 1) load(ub, rb);
+#pragma unroll 1
+    for (int n = 0; n < total; n += 2) {
+        if (!step(n, ua, ra)) return;
+        if (n + 1 < total && !step(n + 1, ub, rb)) return;
     }
 }
 
 __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_constant__ MoeArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    MoeWarp w;
-    w.smem = align1024(smem_raw);
-    w.warp = threadIdx.x >> 5;
-    w.lane = threadIdx.x & 31;
-    const int warp = w.warp, lane = w.lane;
-    float *weight = reinterpret_cast<float *>(w.smem + kMoeWeightAt);
-    unsigned short *choice = reinterpret_cast<unsigned short *>(w.smem + kMoeChoiceAt);
-    unsigned short *order = reinterpret_cast<unsigned short *>(w.smem + kMoeOrderAt);
-    MoeJob *jobs = reinterpret_cast<MoeJob *>(w.smem + kMoeJobAt);
-    int *count = reinterpret_cast<int *>(w.smem + kMoeCountAt);
-    w.jobs = jobs;
-    w.order = order;
-    w.ring = smem_addr(w.smem) + kMoeRingAt + warp * (kMoeStages * kMoeStageBytes);
-    w.cring = smem_addr(w.smem) + kMoeScaleAt + warp * (kMoeStages * kMoeScaleBytes);
-    w.full = smem_addr(w.smem) + kMoeBarAt + warp * (kMoeStages * 8);
-    w.bar = smem_addr(w.smem) + kMoeBarAt + kMoeWarps * kMoeStages * 8;
-    int *flags = reinterpret_cast<int *>(w.smem + kMoeBarAt + kMoeWarps * kMoeStages * 8 + 8);   // abort, jobs
-    w.abort = flags;
-    if (lane < kMoeStages) mbar_init(w.full + 8 * lane, 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    MoeCta c;
+    c.window = smem_raw - smem_addr(smem_raw);
+    float *weight = reinterpret_cast<float *>(c.window + kMoeWeightAt);
+    unsigned short *choice = reinterpret_cast<unsigned short *>(c.window + kMoeChoiceAt);
+    unsigned short *order = reinterpret_cast<unsigned short *>(c.window + kMoeOrderAt);
+    MoeJob *jobs = reinterpret_cast<MoeJob *>(c.window + kMoeJobAt);
+    MoeScratch &scratch = *reinterpret_cast<MoeScratch *>(c.window + kMoeHigh);
+    c.jobs = jobs;
+    c.order = order;
+    c.full = kMoeBarAt;
+    c.done = kMoeBarAt + 8 * kMoeStages;
+    c.go = kMoeBarAt + 16 * kMoeStages;
+    int *flags = reinterpret_cast<int *>(c.window + kMoeBarAt + 16 * kMoeStages + 8);   // abort, jobs
+    c.abort = flags;
     if (threadIdx.x == 0) {
-        mbar_init(w.bar, kMoeWarps);
+        for (int s = 0; s < kMoeStages; ++s) {
+            mbar_init(c.full + 8 * s, 2 + kMoeScalers);      // the copies, the sums before, the constants
+            mbar_init(c.done + 8 * s, kMoeWarps);
+        }
+        mbar_init(c.go, 1);
         flags[0] = 0;
     }
     fence_barrier_init();
     // table word (byte, lane) = fp16 pair (Q[byte >> 4] low half, Q[byte & 15] high half)
     for (int i = threadIdx.x; i < 256 * 8; i += kMoeThreads) {
         const uint32_t v = f16x2_of(a.q[i >> 7], a.q[(i >> 3) & 15]);
-        *reinterpret_cast<uint4 *>(w.smem + (i >> 3) * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
+        *reinterpret_cast<uint4 *>(c.window + kMoeTable + (i >> 3) * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
     }
-    for (int e = threadIdx.x; e < a.E; e += kMoeThreads) count[e] = 0;
+    for (int e = threadIdx.x; e < 2 * a.E; e += kMoeThreads) scratch.tokens[e >> 1][e & 1] = 0u;
     if (threadIdx.x < 3) tma_prefetch_desc(threadIdx.x == 0 ? &a.gate.codes : threadIdx.x == 1 ? &a.up.codes : &a.down.codes);
     griddep_wait();
 
     // ---------------- the chosen experts, the same in every CTA
-    for (int t = warp; t < a.T; t += kMoeWarps) moe_choose(a, t, lane, weight, choice);
     __syncthreads();
+    moe_choose(a, scratch, weight, choice);
     const int slots = a.T * a.k;
-    for (int s = threadIdx.x; s < slots; s += kMoeThreads) {
-        atomicAdd(&count[choice[s]], 1);                     // a count: the order does not matter
-        if (blockIdx.x == 0) {
-            if (a.experts) a.experts[s] = choice[s];
-            if (a.weights) a.weights[s] = weight[s];
-        }
-    }
-    __syncthreads();
     if (warp == 0) {
         // jobs in expert order: exclusive sums of the slots and jobs before an expert, 32 experts at a time
         int s0 = 0, j0 = 0;
+#pragma unroll 1
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane, n = e < a.E ? count[e] : 0, nj = (n + kMoeJobTokens - 1) / kMoeJobTokens;
+            const int e = e0 + lane, n = e < a.E ? __popc(scratch.tokens[e][0]) + __popc(scratch.tokens[e][1]) : 0;
+            const int nj = (n + kMoeJob - 1) / kMoeJob;
             int s = n, j = nj;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -741,47 +859,45 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
             }
             const int first = s0 + s - n;
             for (int q = 0; q < nj; ++q)
-                jobs[j0 + j - nj + q] = {(short)e, (short)(first + q * kMoeJobTokens),
-                                         (short)min(kMoeJobTokens, n - q * kMoeJobTokens), 0};
-            if (e < a.E) count[e] = first;
+                jobs[j0 + j - nj + q] = {(short)e, (short)(first + q * kMoeJob), (short)min(kMoeJob, n - q * kMoeJob), 0};
+            if (e < a.E) scratch.p[e] = __int_as_float(first);
             s0 += __shfl_sync(0xffffffffu, s, 31);
             j0 += __shfl_sync(0xffffffffu, j, 31);
         }
         if (lane == 0) flags[1] = j0;
     }
     __syncthreads();
-    // slots by expert, in slot order: a slot's place is the number of earlier slots of its expert
+    // slots by expert, in token order
     for (int s = threadIdx.x; s < slots; s += kMoeThreads) {
-        const int e = choice[s];
-        int before = 0;
-        for (int q = 0; q < s; ++q) before += choice[q] == e ? 1 : 0;
-        order[count[e] + before] = (unsigned short)s;
+        const int e = choice[s], t = s / a.k;
+        const unsigned lo = scratch.tokens[e][0], hi = scratch.tokens[e][1];
+        const int before = t < 32 ? __popc(lo & ((1u << t) - 1u)) : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1u));
+        order[__float_as_int(scratch.p[e]) + before] = (unsigned short)s;
+        if (blockIdx.x == 0) {
+            if (a.experts) a.experts[s] = e;
+            if (a.weights) a.weights[s] = weight[s];
+        }
     }
+    fence_proxy_async_smem();                                // the copies overwrite the scratch
     __syncthreads();
-    w.njobs = flags[1];
 
     // ---------------- this CTA's share of the two phases
-    const int tg1 = kMoeWarps / a.wk1, tg2 = kMoeWarps / a.wk2;
-    MoePhase p0, p1;
-    p0.per = (a.F / 8 + tg1 - 1) / tg1;
-    p1.per = (a.D / 16 + tg2 - 1) / tg2;
-    const int64_t n0 = (int64_t)w.njobs * a.nck1 * p0.per, n1 = (int64_t)w.njobs * a.nck2 * p1.per, c = blockIdx.x, nc = gridDim.x;
-    p0.begin = (int)(n0 * c / nc);
-    p0.end = (int)(n0 * (c + 1) / nc);
-    p1.begin = (int)(n1 * c / nc);
-    p1.end = (int)(n1 * (c + 1) / nc);
-    w.iphase = 0;
-    w.ileft = p0.end - p0.begin;
-    w.iseg = p0.begin / p0.per;
-    w.igroup = p0.begin - w.iseg * p0.per;
-    w.issued = w.done = w.round = 0;
-    w.dead = false;
-    for (int i = 0; i < kMoeStages; ++i) moe_fill(a, w, p0, p1);
-
-    moe_phase<0>(a, w, p0, p1);
-    grid_barrier(a.counters, w.abort);
-    moe_phase<1>(a, w, p0, p1);
-    grid_barrier(a.counters + 1, w.abort);
+    const MoePhase p0 = moe_share(flags[1], a.nck1, a.nsl1, a.lwk1, a.F, 8, a.D);
+    const MoePhase p1 = moe_share(flags[1], a.nck2, a.nsl2, a.lwk2, a.D, 16, a.F);
+    if (warp < kMoeWarps) moe_multiply(a, c, p0, p1);
+    else if (warp == kMoeWarps) moe_copier(a, c, p0, p1);
+    else if (warp <= kMoeWarps + kMoeAdders) moe_adder(a, c, p0, p1);
+    else moe_scaler(a, c, p0, p1);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (*c.abort) {                                      // a wait ran out: within a limit, let copies under way land
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {
+            }
+        }
+        grid_arrive_wait(a.counters + 1, c.abort);
+    }
+    __syncthreads();
 
     // ---------------- Y[t] = sum over choices in order, each the sum of its chunks in order
     const int d4 = a.D / 4;
@@ -809,10 +925,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
     }
 }
 
+// log2 of the warps along a row of nsl slices
 int moe_along(int nsl) {
-    int wk = kMoeWarps;
-    while (wk > 1 && wk / 2 >= nsl) wk /= 2;
-    return wk;
+    int l = 4;
+    while (l > 0 && (1 << (l - 1)) >= nsl) --l;
+    return l;
 }
 
 struct MoeLayout {
@@ -837,12 +954,18 @@ MoeLayout moe_layout(int64_t T, int64_t D, int64_t F, int64_t E, int64_t k) {
     return l;
 }
 
-bool moe_weight(MoeWeight *w, const NF4View &v, int box_rows) {
+bool moe_weight(MoeWeight *w, const NF4View &v, int rows, int nsl, int nck) {
     w->scale8 = v.scale8;
     w->scale2 = v.scale2;
     w->offset = v.offset;
-    return make_map(&w->codes, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)v.cols / 2, (uint64_t)v.rows,
-                    (uint64_t)v.cols / 2, 128, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (v.cols % kMoeStepK != 0)
+        return make_map(&w->codes, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)v.cols / 2, (uint64_t)v.rows,
+                        (uint64_t)v.cols / 2, 128, (uint32_t)rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint64_t dims[3] = {128, (uint64_t)v.rows, (uint64_t)nsl}, strides[2] = {(uint64_t)v.cols / 2, 128};
+    const uint32_t most = (uint32_t)ceil_div(nsl, nck), least = (uint32_t)std::max(nsl / nck, 1);
+    const uint32_t box[3] = {128, (uint32_t)rows, most}, box_less[3] = {128, (uint32_t)rows, least};
+    return make_map_3d(&w->codes, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map_3d(&w->codes_less, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box_less, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -861,7 +984,6 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     const MoeLayout l = moe_layout(T, D, F, E, k);
     char *p = static_cast<char *>(ws);
     MoeArgs a;
-    if (!moe_weight(&a.gate, gate, 8) || !moe_weight(&a.up, up, 8) || !moe_weight(&a.down, down, 16)) return cudaErrorInvalidValue;
     double *logits = reinterpret_cast<double *>(p + l.logits);
     __half *xq = reinterpret_cast<__half *>(p + l.xq);
     float *xup = reinterpret_cast<float *>(p + l.xup);
@@ -884,16 +1006,24 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     a.nsl2 = (int)ceil_div(F, kMoeStepK);
     a.nck1 = (int)ceil_div(a.nsl1, kMoeWarps);
     a.nck2 = (int)ceil_div(a.nsl2, kMoeWarps);
-    a.wk1 = a.nck1 > 1 ? kMoeWarps : moe_along(a.nsl1);
-    a.wk2 = a.nck2 > 1 ? kMoeWarps : moe_along(a.nsl2);
+    a.lwk1 = moe_along(a.nsl1);
+    a.lwk2 = moe_along(a.nsl2);
+    a.whole1 = D % kMoeStepK == 0;
+    a.whole2 = F % kMoeStepK == 0;
+    if (!moe_weight(&a.gate, gate, 8, a.nsl1, a.nck1) || !moe_weight(&a.up, up, 8, a.nsl1, a.nck1) ||
+        !moe_weight(&a.down, down, 16, a.nsl2, a.nck2))
+        return cudaErrorInvalidValue;
     const Codebook &cb = host_codebook();
     for (int i = 0; i < 16; ++i) a.q[i] = cb.q[i];
     const int sms = num_sms();
     cudaError_t e = set_smem(k_moe_experts, kMoeSmem);
     if (e != cudaSuccess) return e;
+    int reserved = 0, dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess) return e;
+    if (reserved != (int)kMoeLow) return cudaErrorInvalidValue;      // the kernel's addresses are absolute
 
-    const int64_t items = E * ceil_div(T, (int64_t)kRouteTokens) + T * a.nsl1;
-    const int rgrid = (int)std::min<int64_t>(ceil_div(items, (int64_t)(kRouteThreads / 32)), 4 * (int64_t)sms);
+    const int rgrid = (int)(E * ceil_div(T, (int64_t)kRouteTokens) + ceil_div(T * a.nsl1, (int64_t)(kRouteThreads / 32)));
     if (router_f32)
         QNF4_LAUNCH("k_moe_route", st,
                     k_moe_route<true><<<rgrid, kRouteThreads, 0, st>>>(X, router, logits, xq, xup, a.counters, a.T, a.D, a.E, a.nsl1));
