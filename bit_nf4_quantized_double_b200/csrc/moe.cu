@@ -18,9 +18,9 @@
 // one slice of 256 inputs in registers and take tiles of 16 weight rows: eight gate and the eight
 // up rows of the same outputs, or 16 down rows. A code byte becomes an fp16 pair by one permute
 // (byte * 256 + lane * 4 + the table's address) and one load from a table replicated per lane;
-// mma.sync m16n8k16 sums a 64-block, fp32 arithmetic applies its constant. Seven more warps do
+// mma.sync m16n8k16 sums a 64-block, fp32 arithmetic applies its constant. Eight more warps do
 // everything else, in step with the others by two barriers per stage of a ring of four: one
-// copies the codes (TMA), two add the sixteen warps' results in a fixed order, four turn int8
+// copies the codes (TMA), three add the sixteen warps' results in a fixed order, four turn int8
 // constants into c = scale8 (scale2 / 127) + offset. With all of it in the sixteen warps a tile took
 // about 560 instructions of a warp, 200 of them the products.
 //
@@ -42,7 +42,7 @@ using namespace tc;
 namespace {
 
 constexpr int kMoeWarps = 16;                       // that multiply
-constexpr int kMoeScalers = 4, kMoeAdders = 2;
+constexpr int kMoeScalers = 4, kMoeAdders = 3;
 constexpr int kMoeHelpers = 1 + kMoeAdders + kMoeScalers;   // the copies, the sums, the block constants
 constexpr int kMoeThreads = 32 * (kMoeWarps + kMoeHelpers);
 constexpr int kMoeStages = 4;
@@ -236,6 +236,7 @@ __device__ __forceinline__ float exp_f64(double d) {
 constexpr int kMoeBatch = 2048;                      // (token, expert) logits that are ranked at a time
 struct MoeScratch {                                  // of the choice, before the stages are filled
     unsigned long long key[kMoeBatch];
+    unsigned high[kMoeBatch];                        // the keys' upper halves
     float p[kMoeBatch];                              // exp(logit - largest)
     double top[kMoeMaxTokens];                       // largest logit
     unsigned tokens[kMoeMaxExperts][2];              // a bit per token that chose the expert
@@ -249,15 +250,35 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeScratch &sh, flo
     for (int t0 = 0; t0 < a.T; t0 += batch) {
         const int nt = min(batch, a.T - t0), n = nt * E;
         const double *logits = a.logits + (int64_t)t0 * E;
-        for (int i = threadIdx.x; i < n; i += kMoeThreads) sh.key[i] = logit_key(__ldcg(logits + i));
+        for (int i = threadIdx.x; i < n; i += kMoeThreads) {
+            const unsigned long long key = logit_key(__ldcg(logits + i));
+            sh.key[i] = key;
+            sh.high[i] = (unsigned)(key >> 32);
+        }
         __syncthreads();
 #pragma unroll 1
         for (int i = threadIdx.x; i < n; i += kMoeThreads) {
             const int t = i / E, e = i - t * E;
-            const unsigned long long *row = sh.key + t * E, mine = row[e];
-            int rank = 0;
+            const unsigned *row = sh.high + t * E, mine = row[e];
+            int rank = 0, same = 0;
+            if (E % 4 == 0) {
 #pragma unroll 4
-            for (int q = 0; q < E; ++q) rank += row[q] > mine || (row[q] == mine && q < e) ? 1 : 0;
+                for (int q = 0; q < E; q += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(row + q);
+                    rank += (v.x > mine ? 1 : 0) + (v.y > mine ? 1 : 0) + (v.z > mine ? 1 : 0) + (v.w > mine ? 1 : 0);
+                    same += (v.x == mine ? 1 : 0) + (v.y == mine ? 1 : 0) + (v.z == mine ? 1 : 0) + (v.w == mine ? 1 : 0);
+                }
+            } else {
+                for (int q = 0; q < E; ++q) {
+                    rank += row[q] > mine ? 1 : 0;
+                    same += row[q] == mine ? 1 : 0;
+                }
+            }
+            if (same > 1) {                                  // the lower halves and the order of the experts decide
+                const unsigned long long *full = sh.key + t * E, own = full[e];
+#pragma unroll 1
+                for (int q = 0; q < E; ++q) rank += row[q] == mine && (full[q] > own || (full[q] == own && q < e)) ? 1 : 0;
+            }
             if (rank < a.k) {
                 choice[(t0 + t) * a.k + rank] = (unsigned short)e;
                 atomicOr(&sh.tokens[e][(t0 + t) >> 5], 1u << ((t0 + t) & 31));
@@ -557,7 +578,7 @@ __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, 
     }
 }
 
-// ---------------- the seven warps around them
+// ---------------- the eight warps around them
 // Copies of one group's codes. Rows past an expert's last tile are the next expert's or zeros (a group's tiles need not
 // divide the expert): their sums are not used.
 __device__ __forceinline__ void moe_copy(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur, int st) {
@@ -676,17 +697,20 @@ __device__ __forceinline__ void moe_constants(const MoeCta &c, int st, const Moe
 }
 
 // A token's value of one output: the warps' sums, in a fixed order.
+template <int N>
+__device__ __forceinline__ float moe_sum_of(const uint8_t *src) {
+    float v[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = *reinterpret_cast<const float *>(src + q * 1024);
+#pragma unroll
+    for (int o = 1; o < N; o *= 2)
+#pragma unroll
+        for (int q = 0; q < N; q += 2 * o) v[q] += v[q + o];
+    return v[0];
+}
 __device__ __forceinline__ float moe_sum(const uint8_t *src, int act) {
-    if (act == kMoeWarps) {
-        float v[kMoeWarps];
-#pragma unroll
-        for (int q = 0; q < kMoeWarps; ++q) v[q] = *reinterpret_cast<const float *>(src + q * 1024);
-#pragma unroll
-        for (int o = 1; o < kMoeWarps; o *= 2)
-#pragma unroll
-            for (int q = 0; q < kMoeWarps; q += 2 * o) v[q] += v[q + o];
-        return v[0];
-    }
+    if (act == kMoeWarps) return moe_sum_of<kMoeWarps>(src);
+    if (act == 8) return moe_sum_of<8>(src);
     float y = 0.0f;
 #pragma unroll 4
     for (int q = 0; q < act; ++q) y += *reinterpret_cast<const float *>(src + q * 1024);
@@ -722,7 +746,7 @@ __device__ __forceinline__ void moe_sums(const MoeArgs &a, const MoeCta &c, cons
 }
 
 // Group n + 4 follows in the stage of group n once that is done: copied by one warp, its constants made by four; the
-// sums of group n, whose places group n + 4 takes, by one of two warps in turn.
+// sums of group n, whose places group n + 4 takes, by one of three warps in turn.
 __device__ __forceinline__ void moe_copier(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
     const int total = p0.count + p1.count;
     MoeCursor cur;
@@ -738,7 +762,7 @@ __device__ __forceinline__ void moe_copier(const MoeArgs &a, const MoeCta &c, co
 
 __device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
     const int lane = threadIdx.x & 31, h = (threadIdx.x >> 5) - kMoeWarps - 1, total = p0.count + p1.count;
-    // every CTA's hidden values: this CTA's are written once both warps are past its last group of phase 0
+    // every CTA's hidden values: this CTA's are written once these warps are past its last group of phase 0
     auto meet = [&]() {
         named_bar_sync(1, 32 * kMoeAdders);
         if (h == 0 && lane == 0) {
@@ -747,20 +771,22 @@ __device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, con
         }
         __syncwarp();
     };
-    if (lane < kMoeStages && (lane & (kMoeAdders - 1)) == h) mbar_arrive(c.full + 8 * lane);   // no sums before the first use
+    if (h == 0 && lane < kMoeStages) mbar_arrive(c.full + 8 * lane);     // no sums before the first use of a stage
     __syncwarp();
     if (p0.count == 0) meet();
     MoeCursor cur;
     cur.start(p0, p1, c.jobs);
+    int turn = 0;
 #pragma unroll 1
     for (int n = 0; n < total; ++n) {
         const int st = n & (kMoeStages - 1);
-        if ((n & (kMoeAdders - 1)) == h) {
+        if (turn == h) {
             if (!moe_wait(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
             moe_sums(a, c, cur.phase ? p1 : p0, cur, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(c.full + 8 * st);
         }
+        turn = turn + 1 == kMoeAdders ? 0 : turn + 1;
         cur.next(p0, p1, c.jobs);
         if (n == p0.count - 1) meet();
     }
@@ -900,26 +926,35 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
     __syncthreads();
 
     // ---------------- Y[t] = sum over choices in order, each the sum of its chunks in order
-    const int d4 = a.D / 4;
-    for (int64_t i = (int64_t)blockIdx.x * kMoeThreads + threadIdx.x; i < (int64_t)a.T * d4; i += (int64_t)gridDim.x * kMoeThreads) {
-        const int t = (int)(i / d4), d = (int)(i - (int64_t)t * d4);
-        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < a.k; ++j) {
-            const int slot = t * a.k + j;
-            const float4 *src = reinterpret_cast<const float4 *>(a.part + (int64_t)slot * a.nck2 * a.D) + d;
-            float4 s = __ldcg(src);
-            for (int q = 1; q < a.nck2; ++q) {
-                const float4 v = __ldcg(src + (int64_t)q * d4);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
+    const int d4 = a.D / 4, parts = a.k * a.nck2;
+    for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < a.T * d4; i += (int)gridDim.x * kMoeThreads) {
+        const int t = i / d4, d = i - t * d4;
+        const float4 *src = reinterpret_cast<const float4 *>(a.part + (int64_t)t * parts * a.D) + d;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int j = 0, q = 0;
+#pragma unroll 1
+        for (int p = 0; p < parts; p += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int o = 0; o < 8; ++o)
+                if (p + o < parts) v[o] = __ldcg(src + (int64_t)(p + o) * d4);
+#pragma unroll
+            for (int o = 0; o < 8; ++o) {
+                if (p + o >= parts) break;
+                s[0] += v[o].x;
+                s[1] += v[o].y;
+                s[2] += v[o].z;
+                s[3] += v[o].w;
+                if (++q == a.nck2) {
+                    const float wt = weight[t * a.k + j++];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = fmaf(wt, s[e], y[e]);
+                        s[e] = 0.0f;
+                    }
+                    q = 0;
+                }
             }
-            const float wt = weight[slot];
-            y[0] = fmaf(wt, s.x, y[0]);
-            y[1] = fmaf(wt, s.y, y[1]);
-            y[2] = fmaf(wt, s.z, y[2]);
-            y[3] = fmaf(wt, s.w, y[3]);
         }
         reinterpret_cast<uint2 *>(a.Y)[i] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     }
