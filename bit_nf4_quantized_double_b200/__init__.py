@@ -150,13 +150,14 @@ def _stream(stream):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _launch(what: str, fn, device: torch.device, stream, *args):
-    """fn(*args, stream) with `device` current and its status checked. A call made on the current
-    device's current stream, as most are, skips the device switch and the stream object."""
-    if stream is None and _raw_stream is not None and torch.cuda.current_device() == device.index:
-        status = fn(*args, _raw_stream(device.index))
+def _launch(what: str, fn, device: int, stream, *args):
+    """fn(*args, stream) with CUDA device `device` current and its status checked. A call made on the
+    current device's current stream, as most are, skips the device switch and the stream object."""
+    if stream is None and _raw_stream is not None and _get_device() == device:
+        status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _stream(stream))
@@ -179,10 +180,13 @@ def _hold(stream, *tensors):
 _DTYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
 
 
-def _same_device(what: str, device: torch.device, *tensors):
-    """Every tensor of a call lives on one CUDA device."""
-    if device.type != "cuda" or any(t.device != device for t in tensors):
-        raise ValueError(f"{what}: all tensors must be on one CUDA device")
+def _same_device(what: str, *tensors) -> int:
+    """The index of the one CUDA device that every tensor of a call lives on."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != d or not t.is_cuda:
+            raise ValueError(f"{what}: all tensors must be on one CUDA device")
+    return d
 
 
 @dataclass
@@ -400,13 +404,16 @@ def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Te
     if codes.dtype != torch.uint8 or absmax.dtype != torch.float32 or codes.numel() * 2 != rows * cols or \
             absmax.numel() * 64 != rows * cols:
         raise ValueError("qlora_fmt4_linear_fwd: codes (uint8) and absmax (fp32) must hold rows * cols weights")
-    dev = X.device
     if Y is None:
-        Y = torch.empty(M, rows, dtype=out_dtype, device=dev)
+        dev = _same_device("qlora_fmt4_linear_fwd", X, codes, absmax)
+        Y = X.new_empty((M, rows), dtype=out_dtype)
+    else:
+        if Y.shape != (M, rows) or not Y.is_contiguous():
+            raise ValueError("qlora_fmt4_linear_fwd: Y must be a contiguous [M, rows] tensor")
+        dev = _same_device("qlora_fmt4_linear_fwd", X, codes, absmax, Y)
     ydt = _DTYPES.get(Y.dtype)
-    if ydt is None or Y.shape != (M, rows) or not Y.is_contiguous():
-        raise ValueError("qlora_fmt4_linear_fwd: Y must be a contiguous bf16 or fp32 [M, rows] tensor")
-    _same_device("qlora_fmt4_linear_fwd", dev, codes, absmax, Y)
+    if ydt is None:
+        raise ValueError("qlora_fmt4_linear_fwd: Y is bf16 or fp32")
     Xc, cc, ac = X.contiguous(), codes.contiguous(), absmax.contiguous()
     _launch("qlora_fmt4_linear_fwd", lib().qlora_fmt4_linear_fwd, dev, stream, Xc.data_ptr(), M, cc.data_ptr(),
             ac.data_ptr(), rows, cols, f, Y.data_ptr(), ydt)
@@ -496,23 +503,23 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     if rdt is None or router.dim() != 2 or router.shape[1] != X.shape[1]:
         raise ValueError("qlora_moe_fwd: router must be a bf16 or fp32 [E, d] tensor")
     T, d = X.shape
-    E, f, dev = router.shape[0], down.cols, X.device
+    E, f = router.shape[0], down.cols
     if gate.cols != d:
         raise ValueError("qlora_moe_fwd: gate must have d columns")
-    if Y is None:
-        Y = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
-    elif Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous():
+    if Y is not None and (Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous()):
         raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
-    _same_device("qlora_moe_fwd", dev, router, Y, gate.codes, up.codes, down.codes, *(() if ws is None else (ws,)))
+    dev = _same_device("qlora_moe_fwd", X, router, gate.codes, up.codes, down.codes, *(t for t in (Y, ws) if t is not None))
+    if Y is None:
+        Y = X.new_empty((T, d))
+    experts = X.new_empty((T, k), dtype=torch.int32)
+    weights = X.new_empty((T, k), dtype=torch.float32)
     Xc, rc = X.contiguous(), router.contiguous()
-    experts = torch.empty(T, k, dtype=torch.int32, device=dev)
-    weights = torch.empty(T, k, dtype=torch.float32, device=dev)
     L = lib()
-    wsb, wsn = _workspace(L.qlora_moe_fwd_workspace(T, d, f, E, k), dev, ws)
+    wsb, wsn = _workspace(L.qlora_moe_fwd_workspace(T, d, f, E, k), X.device, ws)
     tg, tu, td = gate.ctype(), up.ctype(), down.ctype()
-    _launch("qlora_moe_fwd", L.qlora_moe_fwd, dev, stream, Xc.data_ptr(), T, rc.data_ptr(), rdt, E, ctypes.byref(tg),
-            ctypes.byref(tu), ctypes.byref(td), k, int(renorm), Y.data_ptr(), experts.data_ptr(), weights.data_ptr(),
-            0 if wsb is None else wsb.data_ptr(), wsn)
+    _launch("qlora_moe_fwd", L.qlora_moe_fwd, dev, stream, Xc.data_ptr(), T, rc.data_ptr(), rdt, E, tg, tu, td, k,
+            1 if renorm else 0, Y.data_ptr(), experts.data_ptr(), weights.data_ptr(), 0 if wsb is None else wsb.data_ptr(),
+            wsn)
     _hold(stream, Xc, rc, wsb)
     return Y, experts, weights
 

@@ -1051,7 +1051,8 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     const Codebook &cb = host_codebook();
     for (int i = 0; i < 16; ++i) a.q[i] = cb.q[i];
     const int sms = num_sms();
-    cudaError_t e = set_smem(k_moe_experts, kMoeSmem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = set_smem_once(k_moe_experts, kMoeSmem, ready);
     if (e != cudaSuccess) return e;
     int reserved = 0, dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
