@@ -292,17 +292,13 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     // this lane's codes of block b in a stage: matrix rows g and g + 8 are rows 2 g and 2 g + 1 of the
     // tile, so that a wavefront of 16 lanes reads 32 bytes of four rows of one parity, which the
     // swizzle keeps in different banks (row 2 g + 1: the other 16 bytes, 128 further)
-    const uint8_t *at[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        at[b] = smem + warp * (kF4Stages * kF4StageBytes) + g * 256 + ((b ^ (g & 3)) << 5) + t * 8;
-    const int at_odd = 128 + ((t & 2) ? -16 : 16);
-    const uint8_t *sc = smem + kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes) + g * 32;
+    // (block b: bits 5 and 6 flipped by b)
+    const int at = warp * (kF4Stages * kF4StageBytes) + g * 256 + ((g & 3) << 5) + t * 8;
+    const int sc = kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes) + g * 32;
     // pieces of a buffer: [tiles side by side][tile of the round][warp along the row]
-    uint8_t *mypiece = smem + kF4SumAt + (tw * R * wk + kw) * PIECE;
-    int put[4];                                             // this lane's places: tokens 2 t, 2 t + 1, rows 2 g, 2 g + 1
-#pragma unroll
-    for (int e = 0; e < 4; ++e) put[e] = 4 * f4_sum_at(2 * t + (e & 1), 2 * g + (e >> 1));
+    const int mypiece = kF4SumAt + (tw * R * wk + kw) * PIECE;
+    // this lane's place of token 2 t, row 2 g; the other token flips bit 6, the other row bit 5
+    const int put = 4 * f4_sum_at(2 * t, 2 * g);
 
     // Adds round `round` (tiles i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
     // `act` warps that have a slice, in warp order.
@@ -370,7 +366,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                     }
                     // handed over in the places of this warp's own sums (a pass before has been added)
                     auto stage = [&](int m, int u) {
-                        return reinterpret_cast<uint4 *>(mypiece + (m >> 1) * BUF + (m & 1) * (wk * PIECE) + 16 * u);
+                        return reinterpret_cast<uint4 *>(smem + mypiece + (m >> 1) * BUF + (m & 1) * (wk * PIECE) + 16 * u);
                     };
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -379,7 +375,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 }
             }
             for (int i0 = s0; i0 < s1; i0 += R, ++round) {
-                uint8_t *piece = mypiece + (round & 1) * BUF;
+                const int piece = mypiece + (round & 1) * BUF + put;
                 if (sl < 0 && i0 > s0) add_round(round - 1, i0 - R, i0 - R - s0, R, act, pass == 0);
                 if (sl >= 0) {
                     cp_wait<1>();
@@ -396,16 +392,17 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                         }
                         parity ^= 1u << st;
                         flying &= ~(1u << st);
-                        const float4 f0 = *reinterpret_cast<const float4 *>(sc + st * kF4ScaleBytes);
-                        const float4 f1 = *reinterpret_cast<const float4 *>(sc + st * kF4ScaleBytes + 16);
+                        const float4 f0 = *reinterpret_cast<const float4 *>(smem + sc + st * kF4ScaleBytes);
+                        const float4 f1 = *reinterpret_cast<const float4 *>(smem + sc + st * kF4ScaleBytes + 16);
                         const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
                         float acc[NT][4];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(at[b] + so);
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at[b] + (so + at_odd));
+                            const int ab = (at ^ (b << 5)) + so;
+                            const uint2 u = *reinterpret_cast<const uint2 *>(smem + ab);
+                            const uint2 v = *reinterpret_cast<const uint2 *>(smem + (ab ^ 16) + 128);
                             float cc[NT][4];
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -439,7 +436,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (8 * nt + 2 * t + (e & 1) < mn)
-                                    *reinterpret_cast<float *>(piece + i * wk * PIECE + nt * 512 + put[e]) = acc[nt][e] * up[nt][e & 1];
+                                    *reinterpret_cast<float *>(smem + ((piece + i * wk * PIECE + nt * 512) ^ ((e & 1) << 6) ^ ((e >> 1) << 5))) = acc[nt][e] * up[nt][e & 1];
                     }
                 }
                 __syncwarp();                          // the stages have been read, the sums written
