@@ -74,7 +74,8 @@ constexpr uint32_t kMoeOrderAt = kMoeChoiceAt + kMoeMaxSlots * 2;
 constexpr uint32_t kMoeJobAt = kMoeOrderAt + kMoeMaxSlots * 2;
 constexpr uint32_t kMoeBarAt = kMoeJobAt + kMoeMaxJobs * 8;
 constexpr int kMoeSmem = kMoeHigh + (kMoeStages - 1) * kMoeStageBytes - kMoeLow;
-static_assert(kMoeSmem <= 232448 && kMoeBarAt + 128 <= kMoeTable, "shared memory");
+constexpr uint32_t kMoePhaseAt = kMoeBarAt + 128;
+static_assert(kMoeSmem <= 232448 && kMoePhaseAt + 128 <= kMoeTable, "shared memory");
 
 __device__ __forceinline__ uint32_t stage_at(int st) { return st == 0 ? kMoeLow : kMoeHigh + (st - 1) * kMoeStageBytes; }
 
@@ -500,14 +501,10 @@ __device__ __forceinline__ void moe_tokens(const MoeArgs &a, const MoeCta &c, in
 
 __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // this lane's codes of block b (matrix rows g, g + 8: rows tile_row(g), + 8 of the warp's 16), constants, sums
-    int at[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) at[b] = tile_row(g) * 128 + (((2 * b + (t >> 1)) ^ tile_row(g)) << 4) + (t & 1) * 8;
-    const uint8_t *sc = c.window + kMoeScaleAt + tile_row(g) * kMoeScaleRow + warp * 16;
-    uint8_t *put[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) put[e] = c.window + sum_at(0, warp, 2 * t + (e & 1), g + 8 * (e >> 1));
+    // this lane's codes (matrix rows g, g + 8: rows tile_row(g), + 8 of the warp's 16; block b: bits 5 and 6 flipped
+    // by b), constants, sums (the other token: bit 6 flipped; the other row: bit 5)
+    const uint32_t at = tile_row(g) * 128 + (((t >> 1) ^ tile_row(g)) << 4) + (t & 1) * 8;
+    const uint32_t sc = kMoeScaleAt + tile_row(g) * kMoeScaleRow + warp * 16, put = sum_at(0, warp, 2 * t, g);
     const uint32_t table = kMoeTable | (uint32_t)(lane * 4);
 
     uint32_t xb[32];
@@ -534,14 +531,16 @@ __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, 
                 const int st = n & (kMoeStages - 1);
                 if (!moe_wait(c.full + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
                 if (mine) {
-                    const uint8_t *lo = c.window + stage_at(st) + lo_at, *hi = lo + hi_at;
-                    const float4 f0 = *reinterpret_cast<const float4 *>(sc + st * kMoeScaleBytes);
-                    const float4 f1 = *reinterpret_cast<const float4 *>(sc + st * kMoeScaleBytes + 8 * kMoeScaleRow);
+                    const uint32_t lo = stage_at(st) + lo_at + at;
+                    const uint8_t *scale = c.window + (sc + st * kMoeScaleBytes);
+                    const float4 f0 = *reinterpret_cast<const float4 *>(scale);
+                    const float4 f1 = *reinterpret_cast<const float4 *>(scale + 8 * kMoeScaleRow);
                     const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
                     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(lo + at[b]), v = *reinterpret_cast<const uint2 *>(hi + at[b]);
+                        const uint8_t *code = c.window + (lo ^ (uint32_t)(b << 5));
+                        const uint2 u = *reinterpret_cast<const uint2 *>(code), v = *reinterpret_cast<const uint2 *>(code + hi_at);
                         float cc[4];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -565,7 +564,7 @@ __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, 
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (2 * t + (e & 1) < mn)
-                            *reinterpret_cast<float *>(put[e] + st * (kMoeWarps * 1024)) = acc[e] * up[e & 1];
+                            *reinterpret_cast<float *>(c.window + ((put + st * (kMoeWarps * 1024)) ^ (uint32_t)((e & 1) << 6) ^ (uint32_t)((e >> 1) << 5))) = acc[e] * up[e & 1];
                 }
                 __syncwarp();                                // the stage has been read, the sums written
                 if (lane == 0) mbar_arrive(c.done + 8 * st);
@@ -904,12 +903,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
             if (a.weights) a.weights[s] = weight[s];
         }
     }
+    // ---------------- this CTA's share of the two phases
+    MoePhase *phases = reinterpret_cast<MoePhase *>(c.window + kMoePhaseAt);
+    if (threadIdx.x == 0) phases[0] = moe_share(flags[1], a.nck1, a.nsl1, a.lwk1, a.F, 8, a.D);
+    if (threadIdx.x == 32) phases[1] = moe_share(flags[1], a.nck2, a.nsl2, a.lwk2, a.D, 16, a.F);
     fence_proxy_async_smem();                                // the copies overwrite the scratch
     __syncthreads();
-
-    // ---------------- this CTA's share of the two phases
-    const MoePhase p0 = moe_share(flags[1], a.nck1, a.nsl1, a.lwk1, a.F, 8, a.D);
-    const MoePhase p1 = moe_share(flags[1], a.nck2, a.nsl2, a.lwk2, a.D, 16, a.F);
+    const MoePhase &p0 = phases[0], &p1 = phases[1];
     if (warp < kMoeWarps) moe_multiply(a, c, p0, p1);
     else if (warp == kMoeWarps) moe_copier(a, c, p0, p1);
     else if (warp <= kMoeWarps + kMoeAdders) moe_adder(a, c, p0, p1);
