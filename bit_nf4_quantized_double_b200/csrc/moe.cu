@@ -614,84 +614,80 @@ __device__ __forceinline__ void moe_copy(const MoeArgs &a, const MoeCta &c, cons
     __syncwarp();
 }
 
-// Constants of a group. A unit is four blocks of a row: (tile of the group, row, slice), slices fastest, so that the
-// lanes of a warp read runs of a row; at most 256 units for the lanes of four warps. A unit's place relative to the
-// group's first row is the same in every group of a chunk.
-constexpr int kMoeUnits = (256 + 32 * kMoeScalers - 1) / (32 * kMoeScalers);   // per lane
-struct MoeUnits {
-    int off[kMoeUnits];                                      // first block, relative to the group's first row; -1: none
-    int dst[kMoeUnits];                                      // shared offset in a stage
-    int valid[kMoeUnits];                                    // blocks of the unit that the row has (up to 4)
-    int up, key;                                             // bit i: unit i is a row of the up weight; phase and chunk
+// Constants of a group, sixteen rows of a tile in two halves: gate and up rows, or the first and the last eight. A lane
+// of the four warps has a unit, four blocks of a row, in each: (tile of the group, row, slice), slices fastest, so that
+// the lanes read runs of a row. Its place relative to the half's first row is the same in every group of a chunk.
+static_assert(32 * kMoeScalers >= 8 * kMoeWarps, "a unit per lane and half");
+struct MoeUnit {
+    int off;                                                 // first block, relative to the half's first row; INT_MAX: none
+    int dst;                                                 // shared offset in a stage; 8 rows further for the second half
+    int valid;                                               // blocks of the unit that the row has (up to 4)
+    int key;                                                 // phase and chunk
 };
 struct MoeRaw {
-    uint32_t w[kMoeUnits][2];                                // the aligned words of int8 that hold a unit's blocks
-    float s[kMoeUnits][2];                                   // second-level scales of the unit's first and last block
-    int low;                                                 // the group's first block, low bits
+    uint32_t w[2][2];                                        // the aligned words of int8 that hold a unit's blocks
+    float s[2][2];                                           // second-level scales of the unit's first and last block
+    int low[2];                                              // the half's first block, low bits
 };
 
-__device__ __forceinline__ void moe_units(const MoePhase &p, const MoeCursor &cur, MoeUnits &u) {
-    const int first = cur.first, n = cur.slices, phase = cur.phase, rows = phase ? 16 : 8;
-    const int hl = threadIdx.x - 32 * (kMoeWarps + 1 + kMoeAdders), units = (16 * n) << (4 - p.lwk);
-    u.up = 0;
-#pragma unroll
-    for (int i = 0; i < kMoeUnits; ++i) {
-        const int q = hl + 32 * kMoeScalers * i, rs = q / n, s = q - rs * n, r = rs & 15, side = rs >> 4;
-        u.off[i] = q < units ? (side * rows + (phase ? r : r & 7)) * p.kbs + 4 * (first + s) : -1;
-        u.dst[i] = r * kMoeScaleRow + ((side << p.lwk) + s) * 16;
-        u.up |= (phase == 0 && r >= 8 ? 1 : 0) << i;
-        u.valid[i] = min(4, p.kbs - 4 * (first + s));
-    }
-    u.key = phase * 65536 + cur.chunk;
+__device__ __forceinline__ void moe_unit(const MoePhase &p, const MoeCursor &cur, MoeUnit &u) {
+    const int n = cur.slices, rows = cur.phase ? 16 : 8;
+    const int hl = threadIdx.x - 32 * (kMoeWarps + 1 + kMoeAdders), rs = hl / n, q = hl - rs * n, r = rs & 7, side = rs >> 3;
+    u.off = side < kMoeWarps >> p.lwk ? (side * rows + r) * p.kbs + 4 * (cur.first + q) : 0x7fffffff;
+    u.dst = r * kMoeScaleRow + ((side << p.lwk) + q) * 16;
+    u.valid = min(4, p.kbs - 4 * (cur.first + q));
+    u.key = cur.phase * 65536 + cur.chunk;
 }
 
 // Loads the units of a group (rows past the expert's outputs stay zero: their sums are not used). ALIGNED: rows of a
 // multiple of four blocks, so that a unit is one word, of one second-level group.
 template <bool ALIGNED>
-__device__ __forceinline__ void moe_raw(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur,
-                                        const MoeUnits &u, MoeRaw &raw) {
-    const int64_t base = (int64_t)cur.row * p.kbs;
+__device__ __forceinline__ void moe_raw(const MoeArgs &a, const MoePhase &p, const MoeCursor &cur, const MoeUnit &u, MoeRaw &raw) {
     const int room = (p.width - cur.group * cur.step) * p.kbs;   // blocks to the expert's end
-    raw.low = (int)(base & 255);
-    const MoeWeight &first = cur.phase ? a.down : a.gate;
-    const int8_t *s8[2] = {first.scale8 + (base - (base & 3)), cur.phase ? nullptr : a.up.scale8 + (base - (base & 3))};
-    const float *s2[2] = {first.scale2 + (base >> 8), cur.phase ? nullptr : a.up.scale2 + (base >> 8)};
 #pragma unroll
-    for (int i = 0; i < kMoeUnits; ++i) {
+    for (int i = 0; i < 2; ++i) {
+        const MoeWeight &w = cur.phase ? a.down : i ? a.up : a.gate;
+        const int past = cur.phase && i ? 8 : 0;             // rows
+        const int64_t base = (int64_t)(cur.row + past) * p.kbs;
+        raw.low[i] = (int)(base & 255);
         raw.w[i][0] = raw.w[i][1] = 0u;
         raw.s[i][0] = raw.s[i][1] = 0.0f;
-        if ((unsigned)u.off[i] < (unsigned)room) {
-            const bool up = (u.up >> i) & 1;
-            const int8_t *p8 = up ? s8[1] : s8[0];
-            const float *p2 = up ? s2[1] : s2[0];
-            const int b = raw.low + u.off[i], last = b + u.valid[i] - 1;         // first and last block, from base - low on
-            raw.w[i][0] = __ldg(reinterpret_cast<const unsigned int *>(p8 + (((raw.low & 3) + u.off[i]) & ~3)));
-            raw.s[i][0] = __ldg(p2 + (b >> 8));
-            if (!ALIGNED) {
-                raw.w[i][1] = __ldg(reinterpret_cast<const unsigned int *>(p8 + (((raw.low & 3) + u.off[i] + u.valid[i] - 1) & ~3)));
-                raw.s[i][1] = __ldg(p2 + (last >> 8));
+        if (u.off < room - past * p.kbs) {
+            const int8_t *p8 = w.scale8 + base;
+            const float *p2 = w.scale2 + (base >> 8);
+            const int b = raw.low[i] + u.off;                // the unit's first block, from p2's first on
+            if (ALIGNED) {
+                raw.w[i][0] = __ldg(reinterpret_cast<const unsigned int *>(p8 + u.off));
+            } else {
+                const int lo = (raw.low[i] & 3) + u.off;
+                p8 -= raw.low[i] & 3;
+                raw.w[i][0] = __ldg(reinterpret_cast<const unsigned int *>(p8 + (lo & ~3)));
+                raw.w[i][1] = __ldg(reinterpret_cast<const unsigned int *>(p8 + ((lo + u.valid - 1) & ~3)));
+                raw.s[i][1] = __ldg(p2 + ((b + u.valid - 1) >> 8));
             }
+            raw.s[i][0] = __ldg(p2 + (b >> 8));
         }
     }
 }
 
 template <bool ALIGNED>
-__device__ __forceinline__ void moe_constants(const MoeCta &c, int st, const MoeUnits &u, const MoeRaw &raw, float mu0, float mu1) {
+__device__ __forceinline__ void moe_constants(const MoeCta &c, int st, const MoeUnit &u, const MoeRaw &raw, float mu0, float mu1) {
+    if (u.off == 0x7fffffff) return;
 #pragma unroll
-    for (int i = 0; i < kMoeUnits; ++i) {
-        if (u.off[i] < 0) continue;
-        const int b0 = raw.low + u.off[i];                   // first block, modulo 256 and modulo 4
+    for (int i = 0; i < 2; ++i) {
+        const int b0 = raw.low[i] + u.off;                   // first block, modulo 256 and modulo 4
         const uint32_t w = ALIGNED ? raw.w[i][0] : __funnelshift_r(raw.w[i][0], raw.w[i][1], 8 * (b0 & 3));
-        const float mu = (u.up >> i) & 1 ? mu1 : mu0, s0 = raw.s[i][0] * (1.0f / 127.0f);
+        const float mu = i ? mu1 : mu0, s0 = raw.s[i][0] * (1.0f / 127.0f);
         float v[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             float s = s0;
             if (!ALIGNED && b >= 256 - (b0 & 255)) s = raw.s[i][1] * (1.0f / 127.0f);   // the next second-level group
             v[b] = fmaf((float)(int8_t)(w >> (8 * b)), s, mu);
-            if (!ALIGNED && b >= u.valid[i]) v[b] = 0.0f;
+            if (!ALIGNED && b >= u.valid) v[b] = 0.0f;
         }
-        *reinterpret_cast<float4 *>(c.window + kMoeScaleAt + st * kMoeScaleBytes + u.dst[i]) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(c.window + (kMoeScaleAt + st * kMoeScaleBytes + u.dst + i * 8 * kMoeScaleRow)) =
+            make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -795,24 +791,24 @@ __device__ __forceinline__ void moe_scaler(const MoeArgs &a, const MoeCta &c, co
     const int lane = threadIdx.x & 31, total = p0.count + p1.count;
     const float mu[3] = {__ldg(a.gate.offset), __ldg(a.up.offset), __ldg(a.down.offset)};
     // two groups' constants are loaded ahead, in registers
-    MoeUnits ua, ub;
+    MoeUnit ua, ub;
     MoeRaw ra, rb;
     MoeCursor ahead;
     ahead.start(p0, p1, c.jobs);
     ua.key = ub.key = -1;
-    auto load = [&](MoeUnits &u, MoeRaw &r) {
+    auto load = [&](MoeUnit &u, MoeRaw &r) {
         const MoePhase &p = ahead.phase ? p1 : p0;
-        if (u.key != ahead.phase * 65536 + ahead.chunk) moe_units(p, ahead, u);
-        if (p.kbs & 3) moe_raw<false>(a, c, p, ahead, u, r);
-        else moe_raw<true>(a, c, p, ahead, u, r);
+        if (u.key != ahead.phase * 65536 + ahead.chunk) moe_unit(p, ahead, u);
+        if (p.kbs & 3) moe_raw<false>(a, p, ahead, u, r);
+        else moe_raw<true>(a, p, ahead, u, r);
         ahead.next(p0, p1, c.jobs);
     };
-    auto step = [&](int n, MoeUnits &u, MoeRaw &r) {
+    auto step = [&](int n, MoeUnit &u, MoeRaw &r) {
         const int st = n & (kMoeStages - 1), phase = n >= p0.count;
         if (n >= kMoeStages && !moe_wait(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return false;
-        const float mu0 = phase ? mu[2] : mu[0];
-        if ((phase ? p1 : p0).kbs & 3) moe_constants<false>(c, st, u, r, mu0, mu[1]);
-        else moe_constants<true>(c, st, u, r, mu0, mu[1]);
+        const float mu0 = phase ? mu[2] : mu[0], mu1 = phase ? mu[2] : mu[1];
+        if ((phase ? p1 : p0).kbs & 3) moe_constants<false>(c, st, u, r, mu0, mu1);
+        else moe_constants<true>(c, st, u, r, mu0, mu1);
         __syncwarp();
         if (lane == 0) mbar_arrive(c.full + 8 * st);
         if (n + 2 < total) load(u, r);
