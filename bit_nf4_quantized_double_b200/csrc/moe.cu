@@ -374,15 +374,17 @@ struct MoeCursor {
     }
 };
 
-// This CTA's groups of a phase, an even share.
-__device__ __forceinline__ MoePhase moe_share(int njobs, int nck, int nsl, int lwk, int width, int rows, int cols) {
+// This CTA's groups of a phase: an even share of groups and of the time that a segment's tokens take, `start` groups'
+// worth, which a CTA that begins inside of a segment pays too.
+__device__ __forceinline__ MoePhase moe_share(int njobs, int nck, int nsl, int lwk, int width, int rows, int cols, int start) {
     MoePhase p;
     const int tg = kMoeWarps >> lwk;
     p.per = (width / rows + tg - 1) >> (4 - lwk);
-    const unsigned n = (unsigned)njobs * nck * p.per, nc = gridDim.x, c = blockIdx.x, q = n / nc, r = n - q * nc;
-    const unsigned begin = c * q + min(c, r), seg = begin / p.per;
-    p.count = (int)(q + (c < r ? 1 : 0));
-    p.group = (int)(begin - seg * p.per);
+    const unsigned all = (unsigned)(p.per + start), n = (unsigned)njobs * nck * all, nc = gridDim.x, c = blockIdx.x;
+    const unsigned q = n / nc, r = n - q * nc, x0 = c * q + min(c, r), x1 = x0 + q + (c < r ? 1 : 0);
+    const unsigned seg = x0 / all, last = x1 / all;
+    p.group = max((int)(x0 - seg * all) - start, 0);
+    p.count = (int)(last - seg) * p.per + max((int)(x1 - last * all) - start, 0) - p.group;
     p.job = nck == 1 ? (int)seg : (int)(seg / nck);
     p.chunk = (int)seg - p.job * nck;
     p.nck = nck;
@@ -421,19 +423,15 @@ __device__ __forceinline__ void grid_arrive_wait(unsigned *counter, volatile int
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// Eight hidden values of a slot from input k on.
+// Eight hidden values of a slot from input k on, from the sums of g and u over the chunks of D, in order.
 __device__ __forceinline__ void moe_hidden(const MoeArgs &a, int slot, int k, float (&f)[8]) {
     auto add = [](float (&v)[8], const float *src) {
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src)), y = __ldcg(reinterpret_cast<const float4 *>(src) + 1);
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     };
-    if (a.nck1 == 1) {
-        add(f, a.h + (int64_t)slot * a.F + k);
-        return;
-    }
     float u[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < a.nck1; ++c) {                       // the chunks of D in order
+    for (int c = 0; c < a.nck1; ++c) {
         const float *src = a.h + ((int64_t)slot * a.nck1 + c) * 2 * a.F + k;
         add(f, src);
         add(u, src + a.F);
@@ -475,12 +473,10 @@ __device__ __forceinline__ void moe_tokens(const MoeArgs &a, const MoeCta &c, in
         up[0] = __ldcg(a.xup + (s0 / a.k) * a.nsl1 + sl);
         up[1] = __ldcg(a.xup + (s1 / a.k) * a.nsl1 + sl);
     } else {
-        // lane u converts inputs 8 u .. 8 u + 7 of a token's hidden values; the token's four lanes collect theirs
+        // lane u converts inputs 8 u .. 8 u + 7 of a token's hidden values; the token's four lanes collect theirs. Two
+        // tokens' values are on their way at a time (four of them: spills in the products)
         const int k = sl * kMoeStepK + 8 * lane;
-#pragma unroll 1
-        for (int m = 0; m < job.count; ++m) {
-            float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (k < a.F) moe_hidden(a, c.order[job.first + m], k, f);
+        auto convert = [&](int m, const float (&f)[8]) {
             uint4 o;
             const float s = scale_f16(f, o);
             up[0] = 2 * t == m ? s : up[0];
@@ -494,6 +490,37 @@ __device__ __forceinline__ void moe_tokens(const MoeArgs &a, const MoeCta &c, in
                 xb[4 * i + 1] = g == m ? v1 : xb[4 * i + 1];
                 xb[4 * i + 2] = g == m ? v2 : xb[4 * i + 2];
                 xb[4 * i + 3] = g == m ? v3 : xb[4 * i + 3];
+            }
+        };
+        const bool in = k < a.F;
+        if (a.nck1 == 1) {
+#pragma unroll 1
+            for (int m = 0; m < job.count; m += 2) {
+                float4 v[4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int slot = c.order[job.first + min(m + q, job.count - 1)];
+                    const float4 *src = reinterpret_cast<const float4 *>(a.h + (int64_t)slot * a.F + k);
+                    v[2 * q] = v[2 * q + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (in && (q == 0 || m + q < job.count)) {
+                        v[2 * q] = __ldcg(src);
+                        v[2 * q + 1] = __ldcg(src + 1);
+                    }
+                }
+#pragma unroll 1
+                for (int q = m; q < min(m + 2, job.count); ++q) {
+                    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+                    convert(q, f);
+                    v[0] = v[2];
+                    v[1] = v[3];
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int m = 0; m < job.count; ++m) {
+                float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (in) moe_hidden(a, c.order[job.first + m], k, f);
+                convert(m, f);
             }
         }
     }
@@ -691,51 +718,81 @@ __device__ __forceinline__ void moe_constants(const MoeCta &c, int st, const Moe
     }
 }
 
-// A token's value of one output: the warps' sums, in a fixed order.
+// Adds four neighbouring values of a tile of N warps, in warp order; only the first n of them.
 template <int N>
-__device__ __forceinline__ float moe_sum_of(const uint8_t *src) {
-    float v[N];
+__device__ __forceinline__ void moe_add(const uint8_t *src, float4 &y, int n = N) {
+    float4 v[N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = *reinterpret_cast<const float *>(src + q * 1024);
+    for (int q = 0; q < N; ++q)
+        v[q] = q < n ? *reinterpret_cast<const float4 *>(src + q * 1024) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int o = 1; o < N; o *= 2)
-#pragma unroll
-        for (int q = 0; q < N; q += 2 * o) v[q] += v[q + o];
-    return v[0];
-}
-__device__ __forceinline__ float moe_sum(const uint8_t *src, int act) {
-    if (act == kMoeWarps) return moe_sum_of<kMoeWarps>(src);
-    if (act == 8) return moe_sum_of<8>(src);
-    float y = 0.0f;
-#pragma unroll 4
-    for (int q = 0; q < act; ++q) y += *reinterpret_cast<const float *>(src + q * 1024);
-    return y;
+    for (int q = 0; q < N; ++q) y = make_float4(y.x + v[q].x, y.y + v[q].y, y.z + v[q].z, y.w + v[q].w);
 }
 
-// The sums of one group: hidden values, or partial sums of outputs.
+// The sums of one group: hidden values, or partial sums of outputs. A lane has four neighbouring matrix rows r of a token
+// and a tile; tile_row leaves them two outputs apart.
 __device__ __forceinline__ void moe_sums(const MoeArgs &a, const MoeCta &c, const MoePhase &p, const MoeCursor &cur, int st) {
-    const int lane = threadIdx.x & 31, act = cur.slices, ltg = 4 - p.lwk, log = cur.phase ? 4 : 3;
-    const int total = cur.job.count << (log + ltg), out0 = cur.group * cur.step;
-    // element: row of the tile, tile of the group, token. In phase 0 lanes 0..15 add gate products, lanes 16..31 the up
-    // products of the same outputs.
-    const int half = cur.phase ? 0 : lane >> 4, width = cur.phase ? 32 : 16;
+    const int lane = threadIdx.x & 31, act = cur.slices, ltg = 4 - p.lwk, q = lane & 3;
+    const int total = ((cur.job.count + 1) >> 1) << (3 + ltg), out0 = cur.group * cur.step;
+    const bool few = total == 8;                             // eight lanes have all values: a quarter of the warps for each eight
 #pragma unroll 1
-    for (int e0 = 0; e0 < total; e0 += width) {
-        const int e = e0 + (lane & (width - 1));
-        const int r = e & ((1 << log) - 1), side = (e >> log) & ((1 << ltg) - 1), m = min(e >> (log + ltg), kMoeJob - 1);
-        const int out = out0 + (side << log) + (r & 8) + tile_row(r & 7);
-        const float y = moe_sum(c.window + sum_at(st, side << p.lwk, m, r + 8 * half), act);
-        const float u = cur.phase ? 0.0f : __shfl_xor_sync(0xffffffffu, y, 16);
-        if (half || e >= total || out >= p.width) continue;
-        const int slot = c.order[cur.job.first + m];
-        if (cur.phase) {
-            __stcg(a.part + ((int64_t)slot * a.nck2 + cur.chunk) * a.D + out, y);
-        } else if (a.nck1 == 1) {
-            __stcg(a.h + (int64_t)slot * a.F + out, silu(y) * u);
+    for (int e0 = 0; e0 < total; e0 += 32) {
+        const int e = few ? lane & 7 : e0 + lane, side = (e >> 3) & ((1 << ltg) - 1), m = ((e >> 2) & 1) + 2 * (e >> (3 + ltg));
+        bool in = e < total && m < cur.job.count;
+        const uint8_t *src = c.window + sum_at(st, side << p.lwk, in ? m : 0, 4 * q);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (few) {
+            const int run = (act + 3) >> 2, w = (lane >> 3) * run;
+            moe_add<4>(src + w * 1024, y, min(run, act - w));
+#pragma unroll
+            for (int o = 8; o < 32; o *= 2) {
+                y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+                y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+                y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
+                y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+            }
+            in = in && lane < 8;
         } else {
-            float *dst = a.h + ((int64_t)slot * a.nck1 + cur.chunk) * 2 * a.F + out;
-            __stcg(dst, y);
-            __stcg(dst + a.F, u);
+            int w = 0;
+#pragma unroll 1
+            for (; w + 8 <= act; w += 8) moe_add<8>(src + w * 1024, y);
+            if (act & 4) {
+                moe_add<4>(src + w * 1024, y);
+                w += 4;
+            }
+            if (act & 2) {
+                moe_add<2>(src + w * 1024, y);
+                w += 2;
+            }
+            if (act & 1) moe_add<1>(src + w * 1024, y);
+        }
+        const int slot = c.order[cur.job.first + (in ? m : 0)];
+        if (cur.phase) {
+            // rows 8 (q / 2) + 2 i + (q & 1): the even lane takes the first four of eight, the odd one the others
+            const bool odd = q & 1;
+            const float s0 = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.z, 1), s1 = __shfl_xor_sync(0xffffffffu, odd ? y.y : y.w, 1);
+            const int out = out0 + side * 16 + 4 * q;
+            if (in && out < p.width)
+                __stcg(reinterpret_cast<float4 *>(a.part + ((int64_t)slot * a.nck2 + cur.chunk) * a.D + out),
+                       odd ? make_float4(s0, y.z, s1, y.w) : make_float4(y.x, s0, y.y, s1));
+        } else {
+            // lanes 0 and 1 of four have gate, 2 and 3 up products of the same outputs: half of them each
+            const bool up = q & 2;
+            const float s0 = __shfl_xor_sync(0xffffffffu, up ? y.x : y.z, 2), s1 = __shfl_xor_sync(0xffffffffu, up ? y.y : y.w, 2);
+            const float g0 = up ? s0 : y.x, g1 = up ? s1 : y.y, u0 = up ? y.z : s0, u1 = up ? y.w : s1;
+            const int out = out0 + side * 8 + (up ? 4 : 0) + (q & 1);
+            if (!in || out >= p.width) continue;
+            if (a.nck1 == 1) {
+                float *dst = a.h + (int64_t)slot * a.F + out;
+                __stcg(dst, silu(g0) * u0);
+                __stcg(dst + 2, silu(g1) * u1);
+            } else {
+                float *dst = a.h + ((int64_t)slot * a.nck1 + cur.chunk) * 2 * a.F + out;
+                __stcg(dst, g0);
+                __stcg(dst + 2, g1);
+                __stcg(dst + a.F, u0);
+                __stcg(dst + a.F + 2, u1);
+            }
         }
     }
 }
@@ -901,8 +958,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
     }
     // ---------------- this CTA's share of the two phases
     MoePhase *phases = reinterpret_cast<MoePhase *>(c.window + kMoePhaseAt);
-    if (threadIdx.x == 0) phases[0] = moe_share(flags[1], a.nck1, a.nsl1, a.lwk1, a.F, 8, a.D);
-    if (threadIdx.x == 32) phases[1] = moe_share(flags[1], a.nck2, a.nsl2, a.lwk2, a.D, 16, a.F);
+    // (a segment's tokens take 1.0 to 2.4 us in the first phase, 1.3 to 4 us in the second, a group 1 us)
+    if (threadIdx.x == 0) phases[0] = moe_share(flags[1], a.nck1, a.nsl1, a.lwk1, a.F, 8, a.D, 2);
+    if (threadIdx.x == 32) phases[1] = moe_share(flags[1], a.nck2, a.nsl2, a.lwk2, a.D, 16, a.F, slots >= 6 * flags[1] ? 4 : 2);
     fence_proxy_async_smem();                                // the copies overwrite the scratch
     __syncthreads();
     const MoePhase &p0 = phases[0], &p1 = phases[1];
