@@ -1011,7 +1011,9 @@ def run_profile_case(name, reps=3):
     size, the L2 flushed before each launch): decode1 / decode16 (the decode block's grouped
     forward), layer (one Llama-7B layer quantised and dequantised by the grouped calls),
     adamw (64 M adapter parameters), merge (the 4096^2 adapter merge), fmt4 (the three
-    4-bit reference formats on 2^26 weights), l4096 (one fwd + bwd step of the headline layer),
+    4-bit reference formats on 2^26 weights), fmt4linear (their products of one and of 16 tokens
+    with a [28672, 8192] weight), moe (a layer of 8 experts, two per token, d = 4096, f = 11008,
+    4 tokens), l4096 (one fwd + bwd step of the headline layer),
     l4096fused (the same step through the fused dequant-GEMM kernels)."""
     import torch
     import bit_nf4_quantized_double_b200 as q
@@ -1052,6 +1054,23 @@ def run_profile_case(name, reps=3):
             codes, absmax = q.qlora_fmt4_quantize(W, fmt)
             l2_flush(flush)
             q.qlora_fmt4_dequant(codes, absmax, W.numel(), fmt)
+    elif name == "fmt4linear":
+        rows, cols = 28672, 8192
+        X = si.normal((16, cols), 1.0, seed=78, device="cuda").to(torch.bfloat16)
+        for fmt in ("int4", "fp4_e2m1", "fp4_e3m0"):
+            codes, absmax = q.qlora_fmt4_quantize(si.normal((rows, cols), 0.02, seed=79, device="cuda"), fmt)
+            for M in (1, 16):
+                l2_flush(flush)
+                q.qlora_fmt4_linear_fwd(X[:M], codes, absmax, rows, fmt)
+    elif name == "moe":
+        T, E, k, d, f = 4, 8, 2, 4096, 11008
+        X = si.normal((T, d), 1.0, seed=80, device="cuda").to(torch.bfloat16)
+        router = si.normal((E, d), d ** -0.5, seed=81, device="cuda")
+        gate, up, down = (q.qlora_nf4_quantize(si.normal((n, m), 0.02, seed=82 + i, device="cuda").to(torch.bfloat16))
+                          for i, (n, m) in enumerate(((E * f, d), (E * f, d), (E * d, f))))
+        for _ in range(reps):
+            l2_flush(flush)
+            q.qlora_moe_fwd(X, router, gate, up, down, k)
     elif name == "l4096fused":
         wl, L, inp = headline_inputs(0)
         t = q.qlora_nf4_quantize(inp["W"])
@@ -1090,7 +1109,7 @@ def main():
                     help="only run the decode block at M tokens three times (a small case for ncu) and exit")
     ap.add_argument("--profile-case", default="", metavar="NAME",
                     help="only run a small case for an ncu capture (decode1, decode16, layer, adamw, merge, fmt4, "
-                         "l4096) and exit")
+                         "fmt4linear, moe, l4096, l4096fused) and exit")
     args = ap.parse_args()
     if args.profile_case:
         run_profile_case(args.profile_case)

@@ -145,7 +145,6 @@ __device__ __forceinline__ float scale_f16(const float (&f)[8], uint4 &o) {
 
 // ---------------------------------------------------------------- routing
 constexpr int kRouteThreads = 256;
-constexpr int kRouteTokens = 4;                     // tokens of a CTA
 
 __device__ __forceinline__ void bf16x8(uint4 v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -156,16 +155,18 @@ __device__ __forceinline__ void bf16x8(uint4 v, float (&f)[8]) {
     }
 }
 
-// A CTA per (expert, four tokens): its eight warps take 256 inputs each in turn and add their sums in warp order; then a
+// A CTA per (expert, TOK tokens): its eight warps take 256 inputs each in turn and add their sums in warp order; then a
 // CTA per eight (token, slice) conversions. The router is a few hundred KB, so the kernel is a latency, mostly of fp64
-// additions that wait for one another: with a warp per logit it took 6 to 12 us.
-template <bool F32>
+// additions that wait for one another: with a warp per logit it took 6 to 12 us. TOK is 1 while that leaves at most four
+// CTAs per SM (8 experts, 32 tokens of 4096 inputs: 3.35 us, 5.35 with 4), else 4, which converts the router's values
+// once for four tokens (64 experts, 16 tokens of 2048 inputs: 4.3 us, 5.0 with 1).
+template <bool F32, int TOK>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16 *X, const void *router, double *logits,
                                                              __half *xq, float *xup, unsigned *counters, int T, int D,
                                                              int E, int nsl) {
-    __shared__ double sums[kRouteTokens][kRouteThreads / 32];
+    __shared__ double sums[TOK][kRouteThreads / 32];
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tq = (T + kRouteTokens - 1) / kRouteTokens;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tq = (T + TOK - 1) / TOK;
     if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
     if ((int)blockIdx.x >= E * tq) {
         const int i = ((int)blockIdx.x - E * tq) * (kRouteThreads / 32) + warp, t = i / nsl, s = i - t * nsl;
@@ -179,10 +180,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16
         if (lane == 0) xup[t * nsl + s] = up;
         return;
     }
-    const int e = (int)blockIdx.x / tq, t0 = ((int)blockIdx.x - e * tq) * kRouteTokens;
-    double acc[kRouteTokens][2];
+    const int e = (int)blockIdx.x / tq, t0 = ((int)blockIdx.x - e * tq) * TOK;
+    double acc[TOK][2];
 #pragma unroll
-    for (int i = 0; i < kRouteTokens; ++i) acc[i][0] = acc[i][1] = 0.0;
+    for (int i = 0; i < TOK; ++i) acc[i][0] = acc[i][1] = 0.0;
 #pragma unroll 2
     for (int k = 256 * warp + 8 * lane; k < D; k += 8 * kRouteThreads) {
         float r[8];
@@ -195,8 +196,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16
             bf16x8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(router) + (int64_t)e * D + k)), r);
         }
 #pragma unroll
-        for (int i = 0; i < kRouteTokens; ++i) {
-            if (t0 + i >= T) break;
+        for (int i = 0; i < TOK; ++i) {
+            if (TOK > 1 && t0 + i >= T) break;
             float x[8];
             bf16x8(__ldg(reinterpret_cast<const uint4 *>(X + (int64_t)(t0 + i) * D + k)), x);
 #pragma unroll
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16
         }
     }
 #pragma unroll
-    for (int i = 0; i < kRouteTokens; ++i) {
+    for (int i = 0; i < TOK; ++i) {
         if (t0 + i >= T) break;
         double v = acc[i][0] + acc[i][1];
 #pragma unroll
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __nv_bfloat16
         if (lane == 0) sums[i][warp] = v;
     }
     __syncthreads();
-    if (threadIdx.x < kRouteTokens && t0 + (int)threadIdx.x < T) {
+    if (threadIdx.x < TOK && t0 + (int)threadIdx.x < T) {
         double v = 0.0;
 #pragma unroll
         for (int w = 0; w < kRouteThreads / 32; ++w) v += sums[threadIdx.x][w];
@@ -814,7 +815,8 @@ __device__ __forceinline__ void moe_copier(const MoeArgs &a, const MoeCta &c, co
 
 __device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, const MoePhase &p0, const MoePhase &p1) {
     const int lane = threadIdx.x & 31, h = (threadIdx.x >> 5) - kMoeWarps - 1, total = p0.count + p1.count;
-    // every CTA's hidden values: this CTA's are written once these warps are past its last group of phase 0
+    // every CTA's hidden values: this CTA's are written once these warps are past its last group of phase 0, or have
+    // given up (all three come here, so that none waits for another without a limit)
     auto meet = [&]() {
         named_bar_sync(1, 32 * kMoeAdders);
         if (h == 0 && lane == 0) {
@@ -833,7 +835,10 @@ __device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, con
     for (int n = 0; n < total; ++n) {
         const int st = n & (kMoeStages - 1);
         if (turn == h) {
-            if (!moe_wait(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
+            if (!moe_wait(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) {
+                if (n < p0.count) meet();
+                return;
+            }
             moe_sums(a, c, cur.phase ? p1 : p0, cur, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(c.full + 8 * st);
@@ -1113,13 +1118,12 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     if ((e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess) return e;
     if (reserved != (int)kMoeLow) return cudaErrorInvalidValue;      // the kernel's addresses are absolute
 
-    const int rgrid = (int)(E * ceil_div(T, (int64_t)kRouteTokens) + ceil_div(T * a.nsl1, (int64_t)(kRouteThreads / 32)));
-    if (router_f32)
-        QNF4_LAUNCH("k_moe_route", st,
-                    k_moe_route<true><<<rgrid, kRouteThreads, 0, st>>>(X, router, logits, xq, xup, a.counters, a.T, a.D, a.E, a.nsl1));
-    else
-        QNF4_LAUNCH("k_moe_route", st,
-                    k_moe_route<false><<<rgrid, kRouteThreads, 0, st>>>(X, router, logits, xq, xup, a.counters, a.T, a.D, a.E, a.nsl1));
+    const int tok = E * T <= 4 * sms ? 1 : 4;
+    const int rgrid = (int)(E * ceil_div(T, (int64_t)tok) + ceil_div(T * a.nsl1, (int64_t)(kRouteThreads / 32)));
+    const auto route = router_f32 ? (tok == 1 ? k_moe_route<true, 1> : k_moe_route<true, 4>)
+                                  : (tok == 1 ? k_moe_route<false, 1> : k_moe_route<false, 4>);
+    QNF4_LAUNCH("k_moe_route", st,
+                route<<<rgrid, kRouteThreads, 0, st>>>(X, router, logits, xq, xup, a.counters, a.T, a.D, a.E, a.nsl1));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     cudaLaunchConfig_t cfg{};
