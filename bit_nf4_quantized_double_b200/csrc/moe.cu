@@ -228,6 +228,10 @@ __device__ __forceinline__ unsigned long long logit_key(double v) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(v);
     return (b >> 63) ? ~b : b | (1ull << 63);
 }
+// The logit of a key (NaN for every NaN, +0 for -0).
+__device__ __forceinline__ double key_logit(unsigned long long k) {
+    return __longlong_as_double((long long)((k >> 63) ? k ^ (1ull << 63) : ~k));
+}
 // exp(d) for d <= 0: the part of d that fp32 drops enters as its first-order term.
 __device__ __forceinline__ float exp_f64(double d) {
     const float hi = (float)d;
@@ -285,11 +289,11 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeScratch &sh, flo
                 choice[(t0 + t) * a.k + rank] = (unsigned short)e;
                 atomicOr(&sh.tokens[e][(t0 + t) >> 5], 1u << ((t0 + t) & 31));
             }
-            if (rank == 0) sh.top[t0 + t] = __ldcg(logits + i);
+            if (rank == 0) sh.top[t0 + t] = key_logit(sh.key[i]);
         }
         __syncthreads();
 #pragma unroll 1
-        for (int i = threadIdx.x; i < n; i += kMoeThreads) sh.p[i] = exp_f64(__ldcg(logits + i) - sh.top[t0 + i / E]);
+        for (int i = threadIdx.x; i < n; i += kMoeThreads) sh.p[i] = exp_f64(key_logit(sh.key[i]) - sh.top[t0 + i / E]);
         __syncthreads();
         // weights: a warp per token
 #pragma unroll 1
