@@ -406,7 +406,7 @@ def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Te
         raise ValueError("qlora_fmt4_linear_fwd: codes (uint8) and absmax (fp32) must hold rows * cols weights")
     if Y is None:
         dev = _same_device("qlora_fmt4_linear_fwd", X, codes, absmax)
-        Y = X.new_empty((M, rows), dtype=out_dtype)
+        Y = torch.empty_strided((M, rows), (rows, 1), dtype=out_dtype, device=X.device)
     else:
         if Y.shape != (M, rows) or not Y.is_contiguous():
             raise ValueError("qlora_fmt4_linear_fwd: Y must be a contiguous [M, rows] tensor")
@@ -509,11 +509,12 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     if Y is not None and (Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous()):
         raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
     dev = _same_device("qlora_moe_fwd", X, router, gate.codes, up.codes, down.codes, *(t for t in (Y, ws) if t is not None))
-    if Y is None:
-        Y = X.new_empty((T, d))
-    experts = X.new_empty((T, k), dtype=torch.int32)
-    weights = X.new_empty((T, k), dtype=torch.float32)
     Xc, rc = X.contiguous(), router.contiguous()
+    if Y is None:
+        Y = torch.empty_like(Xc)
+    # empty_strided is the cheapest of torch's allocations, a tenth of this call's host time
+    experts = torch.empty_strided((T, k), (k, 1), dtype=torch.int32, device=X.device)
+    weights = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=X.device)
     L = lib()
     wsb, wsn = _workspace(L.qlora_moe_fwd_workspace(T, d, f, E, k), X.device, ws)
     tg, tu, td = gate.ctype(), up.ctype(), down.ctype()

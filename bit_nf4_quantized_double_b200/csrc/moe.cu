@@ -1062,8 +1062,12 @@ bool moe_weight(MoeWeight *w, const NF4View &v, int rows, int nsl, int nck) {
     const uint64_t dims[3] = {128, (uint64_t)v.rows, (uint64_t)nsl}, strides[2] = {(uint64_t)v.cols / 2, 128};
     const uint32_t most = (uint32_t)ceil_div(nsl, nck), least = (uint32_t)std::max(nsl / nck, 1);
     const uint32_t box[3] = {128, (uint32_t)rows, most}, box_less[3] = {128, (uint32_t)rows, least};
-    return make_map_3d(&w->codes, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           make_map_3d(&w->codes_less, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box_less, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!make_map_3d(&w->codes, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
+    if (most == least) {                                     // every chunk the same: not used
+        w->codes_less = w->codes;
+        return true;
+    }
+    return make_map_3d(&w->codes_less, v.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, strides, box_less, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -1117,10 +1121,14 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = set_smem_once(k_moe_experts, kMoeSmem, ready);
     if (e != cudaSuccess) return e;
-    int reserved = 0, dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess) return e;
-    if (reserved != (int)kMoeLow) return cudaErrorInvalidValue;      // the kernel's addresses are absolute
+    static std::atomic<bool> window{false};                  // the kernel's shared addresses are absolute
+    if (!window.load(std::memory_order_relaxed)) {
+        int reserved = 0, dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess) return e;
+        if (reserved != (int)kMoeLow) return cudaErrorInvalidValue;
+        window.store(true, std::memory_order_relaxed);
+    }
 
     const int tok = E * T <= 4 * sms ? 1 : 4;
     const int rgrid = (int)(E * ceil_div(T, (int64_t)tok) + ceil_div(T * a.nsl1, (int64_t)(kRouteThreads / 32)));
