@@ -65,7 +65,7 @@ constexpr int kF4SumAt = kF4ScaleAt + kF4Warps * kF4Stages * kF4ScaleBytes;
 __host__ __device__ constexpr int f4_piece(int nt) { return 16 * 8 * nt * 4; }          // a warp's sums of a tile
 __host__ __device__ constexpr int f4_buf_bytes(int nt) { return kF4Round * kF4Warps * f4_piece(nt); }
 __host__ __device__ constexpr int f4_bar_at(int nt) { return kF4SumAt + 2 * f4_buf_bytes(nt); }
-__host__ __device__ constexpr int f4_seg_at(int nt) { return f4_bar_at(nt) + kF4Warps * kF4Stages * 8 + 32; }
+__host__ __device__ constexpr int f4_seg_at(int nt) { return f4_bar_at(nt) + kF4Warps * 16 + 32; }
 __host__ __device__ constexpr int f4_seg_tiles(int nt) { return 32 / nt; }
 constexpr int f4_smem(int nt, bool cluster) { return 1024 + f4_seg_at(nt) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0); }
 static_assert(f4_smem(1, true) <= 232448 && f4_smem(2, true) <= 232448, "shared memory");
@@ -77,8 +77,8 @@ __device__ __forceinline__ int f4_sum_at(int m, int r) {
 }
 
 struct F4Args {
-    CUtensorMap codes;         // bytes [rows, K / 2], box of a step, 128-byte swizzle
-    CUtensorMap scales;        // fp32 [rows, K / 64], box of a step (vec_scales)
+    // bytes [rows, K / 2], boxes of a round and of a step, 128-byte swizzle; fp32 [rows, K / 64] likewise (vec_scales)
+    CUtensorMap codes, codes_step, scales, scales_step;
     const __nv_bfloat16 *X;
     const float *absmax;
     void *Y;
@@ -234,12 +234,12 @@ __device__ __forceinline__ bool f4_wait(uint32_t bar, uint32_t parity, volatile 
     return mbar_try_wait(bar, parity) || f4_wait_slow(bar, parity, abort);
 }
 
-// Before an early exit: waits, within a limit, for the copies of the stages in `flying`.
-__device__ __noinline__ void f4_drain(uint32_t full, uint32_t flying, uint32_t parity) {
+// Before an early exit: waits, within a limit, for the copies of rounds `used` .. `filled` - 1.
+__device__ __noinline__ void f4_drain(uint32_t full, uint32_t used, uint32_t filled) {
     cp_wait<0>();
     const uint64_t t0 = global_timer_ns();
-    for (int s = 0; s < kF4Stages; ++s)
-        while (((flying >> s) & 1u) && !mbar_try_wait(full + 8 * s, (parity >> s) & 1u))
+    for (; used != filled; ++used)
+        while (!mbar_try_wait(full + 8 * (used & 1u), (used >> 1) & 1u))
             if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * (kF4Stages * kF4StageBytes);
     const uint32_t cring = smem_addr(smem) + kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes);
-    const uint32_t full = smem_addr(smem) + f4_bar_at(NT) + warp * (kF4Stages * 8);
-    const uint32_t bar = smem_addr(smem) + f4_bar_at(NT) + kF4Warps * kF4Stages * 8;   // a round's sums are written
-    volatile int *abort = reinterpret_cast<int *>(smem + f4_bar_at(NT) + kF4Warps * kF4Stages * 8 + 8);
+    const uint32_t full = smem_addr(smem) + f4_bar_at(NT) + warp * 16;               // the ring's two rounds
+    const uint32_t bar = smem_addr(smem) + f4_bar_at(NT) + kF4Warps * 16;   // a round's sums are written
+    volatile int *abort = reinterpret_cast<int *>(smem + f4_bar_at(NT) + kF4Warps * 16 + 8);
     float *seg = reinterpret_cast<float *>(smem + f4_seg_at(NT));
-    if (lane < kF4Stages) mbar_init(full + 8 * lane, 1);
+    if (lane < 2) mbar_init(full + 8 * lane, 1);
     if (threadIdx.x == 0) {
         mbar_init(bar, kF4Warps);
         *abort = 0;
@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     const int rank = CLUSTER ? (int)cluster_ctarank() : 0;
     const int ncl = gridDim.x / nch, cl = blockIdx.x / nch;
     const int groups = (int)((a.N + kF4StepRows * tg - 1) / (kF4StepRows * tg));
-    const int mine = (groups - cl + ncl - 1) / ncl;        // tile groups cl, cl + ncl, ...
+    // this cluster's tile groups, side by side, so that a copy fetches a round of them
+    const int mine = groups / ncl + (cl < groups % ncl ? 1 : 0), first = cl * (groups / ncl) + min(cl, groups % ncl);
     const int64_t m0 = (int64_t)blockIdx.y * kF4Tokens;
     const int mn = (int)min((int64_t)kF4Tokens, a.M - m0);
     // the row's slices, spread evenly over passes x CTAs
@@ -300,9 +301,9 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     // this lane's place of token 2 t, row 2 g; the other token flips bit 6, the other row bit 5
     const int put = 4 * f4_sum_at(2 * t, 2 * g);
 
-    // Adds round `round` (tiles i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
+    // Adds round `round` (tile groups i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
     // `act` warps that have a slice, in warp order.
-    auto add_round = [&](int round, int i0, int sg, int rn, int act, bool first) {
+    auto add_round = [&](int round, int i0, int sg, int rn, int act, bool fresh) {
         if (!f4_wait(bar, round & 1, abort)) return;
         const uint8_t *buf = smem + kF4SumAt + (round & 1) * BUF;
         for (int e = threadIdx.x; e < tg * R * 128 * NT; e += kF4Threads) {
@@ -323,9 +324,9 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
             }
             if (CLUSTER) {
                 float *dst = seg + (sg + i) * (128 * NT) + o;
-                *dst = first ? y : *dst + y;
+                *dst = fresh ? y : *dst + y;
             } else {
-                const int row = (cl + (i0 + i) * ncl) * (tg * kF4StepRows) + (ti / R) * kF4StepRows + r;
+                const int row = ((first + i0) * tg + (ti / R) * rn + i) * kF4StepRows + r;
                 if (row < (int)a.N) f4_store(a, m0 + m, row, y);
             }
         }
@@ -334,19 +335,23 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     const int seg_len = CLUSTER ? f4_seg_tiles(NT) : mine;
     uint32_t xb[NT][32];
     float up[NT][2];
-    uint32_t parity = 0, flying = 0;                        // per stage: phase to wait for; copies under way
+    uint32_t used = 0, filled = 0;                          // rounds of this warp's ring
     int round = 0, sl = -1, act = 0;
     bool dead = false;                                      // a wait ran out
-    // Fills stage i % S with tile i (lane 0; the constants by every lane where TMA cannot)
-    auto fill = [&](int i) {
-        const int st = i & (kF4Stages - 1), row0 = ((cl + i * ncl) * tg + tw) * kF4StepRows;
+    // Fills the other half of the ring with the round of group i, of rn groups: the warp's rn neighbouring tiles (lane 0;
+    // the constants by every lane where TMA cannot)
+    auto fill = [&](int i, int rn) {
+        const int h = (int)(filled & 1u), row0 = ((first + i) * tg + tw * rn) * kF4StepRows;
         if (lane == 0) {
-            mbar_arrive_expect_tx(full + 8 * st, kF4StageBytes + (VEC ? kF4ScaleBytes : 0));
-            tma_load_2d(ring + st * kF4StageBytes, &a.codes, full + 8 * st, sl * 128, row0);
-            if (VEC) tma_load_2d(cring + st * kF4ScaleBytes, &a.scales, full + 8 * st, sl * 4, row0);
+            const uint32_t codes = ring + h * (R * kF4StageBytes), scales = cring + h * (R * kF4ScaleBytes);
+            mbar_arrive_expect_tx(full + 8 * h, rn * (kF4StageBytes + (VEC ? kF4ScaleBytes : 0)));
+            tma_load_2d(codes, rn == R ? &a.codes : &a.codes_step, full + 8 * h, sl * 128, row0);
+            if (VEC) tma_load_2d(scales, rn == R ? &a.scales : &a.scales_step, full + 8 * h, sl * 4, row0);
         }
-        if (!VEC) f4_scales(a, cring + st * kF4ScaleBytes, row0, sl, lane);
-        flying |= 1u << st;
+        if (!VEC)
+            for (int q = 0; q < rn; ++q)
+                f4_scales(a, cring + (h * R + q) * kF4ScaleBytes, row0 + q * kF4StepRows, sl, lane);
+        ++filled;
     };
 
     for (int s0 = 0; s0 < mine; s0 += seg_len) {
@@ -360,9 +365,9 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 sl = kw < act && !dead ? p * sq + min(p, srem) + kw : -1;
                 if (sl >= 0) {
 #pragma unroll
-                    for (int i = 0; i < kF4Stages; ++i) {
-                        if (s0 + i < ahead) fill(s0 + i);
-                        if ((i & (R - 1)) == R - 1) cp_commit();
+                    for (int i = 0; i < kF4Stages; i += R) {
+                        if (s0 + i < ahead) fill(s0 + i, min(R, ahead - s0 - i));
+                        cp_commit();
                     }
                     // handed over in the places of this warp's own sums (a pass before has been added)
                     auto stage = [&](int m, int u) {
@@ -380,29 +385,28 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 if (sl >= 0) {
                     cp_wait<1>();
                     if (!VEC) __syncwarp();
+                    const int h = (int)(used & 1u);
+                    const bool landed = f4_wait(full + 8 * h, (used >> 1) & 1u, abort);
+                    if (!landed) {
+                        f4_drain(full, used, filled);         // the CTA goes on without this warp's slices
+                        dead = true;
+                        sl = -1;
+                    }
+                    ++used;
+                    const int base = at + h * (R * kF4StageBytes), scale = sc + h * (R * kF4ScaleBytes);
 #pragma unroll
                     for (int i = 0; i < R; ++i) {
-                        if (i0 + i >= s1) break;
-                        const int st = (i0 + i) & (kF4Stages - 1), so = st * kF4StageBytes;
-                        if (!f4_wait(full + 8 * st, (parity >> st) & 1u, abort)) {
-                            f4_drain(full, flying, parity);   // the CTA goes on without this warp's slices
-                            dead = true;
-                            sl = -1;
-                            break;
-                        }
-                        parity ^= 1u << st;
-                        flying &= ~(1u << st);
-                        const float4 f0 = *reinterpret_cast<const float4 *>(smem + sc + st * kF4ScaleBytes);
-                        const float4 f1 = *reinterpret_cast<const float4 *>(smem + sc + st * kF4ScaleBytes + 16);
+                        if (!landed || i0 + i >= s1) break;
+                        const float4 f0 = *reinterpret_cast<const float4 *>(smem + scale + i * kF4ScaleBytes);
+                        const float4 f1 = *reinterpret_cast<const float4 *>(smem + scale + i * kF4ScaleBytes + 16);
                         const float c0[4] = {f0.x, f0.y, f0.z, f0.w}, c1[4] = {f1.x, f1.y, f1.z, f1.w};
                         float acc[NT][4];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const int ab = (at ^ (b << 5)) + so;
-                            const uint2 u = *reinterpret_cast<const uint2 *>(smem + ab);
-                            const uint2 v = *reinterpret_cast<const uint2 *>(smem + (ab ^ 16) + 128);
+                            const uint2 u = *reinterpret_cast<const uint2 *>(smem + (base ^ (b << 5)) + i * kF4StageBytes);
+                            const uint2 v = *reinterpret_cast<const uint2 *>(smem + (base ^ (b << 5) ^ 16) + 128 + i * kF4StageBytes);
                             float cc[NT][4];
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -442,9 +446,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 __syncwarp();                          // the stages have been read, the sums written
                 if (lane == 0) mbar_arrive(bar);
                 if (sl >= 0) {
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        if (i0 + i + kF4Stages < ahead) fill(i0 + i + kF4Stages);
+                    if (i0 + kF4Stages < ahead) fill(i0 + kF4Stages, min(R, ahead - i0 - kF4Stages));
                     cp_commit();
                 }
             }
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
             const uint32_t base = smem_addr(seg);
             for (int e = rank * kF4Threads + threadIdx.x; e < (s1 - s0) * 128 * NT; e += nch * kF4Threads) {
                 const int i = e / (128 * NT), o = e & (128 * NT - 1), m = o >> 4;
-                const int64_t row = (int64_t)(cl + (s0 + i) * ncl) * kF4StepRows + (o & 15);
+                const int64_t row = (int64_t)(first + s0 + i) * kF4StepRows + (o & 15);
                 if (m >= mn || row >= a.N) continue;
                 float y = 0.0f;
                 for (int c = 0; c < nch; ++c) y += ld_cluster_f32(map_to_rank(base + 4 * e, c));
@@ -524,9 +526,10 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
                                int64_t cols, qlora_fmt4 f, void *Y, bool y_f32, cudaStream_t st) {
     F4Args a;
     a.X = X;
-    if (!make_map(&a.codes, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)cols / 2, (uint64_t)rows, (uint64_t)cols / 2, 128,
-                  kF4StepRows, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
+    for (int one : {0, 1})
+        if (!make_map(one ? &a.codes_step : &a.codes, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)cols / 2, (uint64_t)rows,
+                      (uint64_t)cols / 2, 128, (one ? 1 : kF4Round) * kF4StepRows, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
     a.absmax = absmax;
     a.Y = Y;
     a.M = M;
@@ -542,9 +545,11 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
     a.vec_scales = a.kbs % 4 == 0 && aligned16(absmax);
     // Int4 operands are m 2^-16; an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7)
     a.factor = f == QLORA_FMT4_INT4 ? 65536.0f / 7.0f : f == QLORA_FMT4_FP4_E2M1 ? 1.0f / 6.0f : 0.0625f;
-    if (a.vec_scales && !make_map(&a.scales, absmax, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)a.kbs, (uint64_t)rows,
-                                  (uint64_t)a.kbs * 4, 4, kF4StepRows, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
+    for (int one : {0, 1})
+        if (a.vec_scales &&
+            !make_map(one ? &a.scales_step : &a.scales, absmax, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)a.kbs, (uint64_t)rows,
+                      (uint64_t)a.kbs * 4, 4, (one ? 1 : kF4Round) * kF4StepRows, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
     // CTAs along a row: enough for a slice per warp, more while there are fewer tiles than SMs
     const int64_t tiles = ceil_div(rows, (int64_t)kF4StepRows);
     int64_t nch = ceil_div(a.nsl, kF4Warps);
