@@ -10,6 +10,8 @@ Entry points (same names as the C ABI):
     qlora_nf4_dequant(q)                     -> bf16 [rows, cols]
     qlora_linear_fwd(X, q, A, B, s)          -> (Y, XA)
     qlora_linear_bwd(X, dY, q, A, B, s, XA)  -> (dX, dA, dB)
+    qlora_fmt4_linear_fwd(X, codes, absmax, rows, fmt)            -> Y, weight in an Int4 / FP4 format
+    qlora_moe_fwd(X, router, gate, up, down, k)                   -> (Y, experts, weights), NF4 experts
     qlora_get_device_status()                -> status code (0 = ok)
 """
 from __future__ import annotations

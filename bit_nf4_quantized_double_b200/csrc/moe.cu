@@ -22,7 +22,14 @@
 // everything else, in step with the others by two barriers per stage of a ring of four: one
 // copies the codes (TMA), three add the sixteen warps' results in a fixed order, four turn int8
 // constants into c = scale8 (scale2 / 127) + offset. With all of it in the sixteen warps a tile took
-// about 560 instructions of a warp, 200 of them the products.
+// about 560 instructions of a warp, 200 of them the products. 24 warps leave 80 registers, 32 of
+// them tokens: what the roles share (shares of the phases, lists) stays in shared memory, since
+// every spill in the products costs (147 instead of 127 us for the second case below).
+//
+// Measured, (T, E, k, d, f): (1, 8, 2, 4096, 11008) 52 us, (4, ...) 121, (32, ...) 214, floors of
+// 21 / 58 / 85 at the measured copy rate; (1, 64, 8, 2048, 1024) 25 us, (16, ...) 70. About 16 us
+// are fixed: logits, choice (2.5 to 5.5), two grid barriers (1.2 each), first copies, last sums. A
+// group of 16 warps' tiles, 32 KB, takes 1.0 us (0.74 at the copy rate).
 //
 // Roundings besides fp32: the codebook to fp16 (2^-11 relative; bf16 would be 2^-8, as much as
 // the output's own), the tokens to fp16 after scaling by a power of two per token and 256 inputs
