@@ -419,7 +419,7 @@ def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Te
     Xc, cc, ac = X.contiguous(), codes.contiguous(), absmax.contiguous()
     _launch("qlora_fmt4_linear_fwd", lib().qlora_fmt4_linear_fwd, dev, stream, Xc.data_ptr(), M, cc.data_ptr(),
             ac.data_ptr(), rows, cols, f, Y.data_ptr(), ydt)
-    _hold(stream, Xc, cc, ac)
+    _hold(stream, Xc, cc, ac, Y)
     return Y
 
 
@@ -508,6 +508,8 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     E, f = router.shape[0], down.cols
     if gate.cols != d:
         raise ValueError("qlora_moe_fwd: gate must have d columns")
+    if k < 0:
+        raise ValueError("qlora_moe_fwd: k must be positive")
     if Y is not None and (Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous()):
         raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
     dev = _same_device("qlora_moe_fwd", X, router, gate.codes, up.codes, down.codes, *(t for t in (Y, ws) if t is not None))
@@ -523,7 +525,7 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     _launch("qlora_moe_fwd", L.qlora_moe_fwd, dev, stream, Xc.data_ptr(), T, rc.data_ptr(), rdt, E, tg, tu, td, k,
             1 if renorm else 0, Y.data_ptr(), experts.data_ptr(), weights.data_ptr(), 0 if wsb is None else wsb.data_ptr(),
             wsn)
-    _hold(stream, Xc, rc, wsb)
+    _hold(stream, Xc, rc, wsb, Y, experts, weights)
     return Y, experts, weights
 
 

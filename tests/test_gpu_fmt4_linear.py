@@ -180,3 +180,20 @@ def test_large_offsets():
     Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, "int4", out_dtype=torch.float32)
     assert (Y[:, :-tail] == 0).all()
     check(Y[:, -tail:].contiguous(), X, codes[-tail * cols // 2:], absmax[-tail * cols // 64:], tail, "int4")
+
+
+def test_output_of_another_stream_is_not_reused():
+    # torch allocates Y on the current stream; dropped while the other stream still writes it, its block must not be
+    # handed out again
+    M, rows, cols = 5, 997, 512
+    X, codes, absmax = inputs(M, rows, cols, seed=17)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, "int4", stream=s)
+    used = Y.data_ptr()
+    del Y
+    fresh = torch.empty(M, rows, dtype=torch.bfloat16, device="cuda")
+    assert fresh.data_ptr() != used
+    s.synchronize()

@@ -207,3 +207,21 @@ def test_decode_step_with_quantised_weights():
     assert (err <= 1.01 * 2.0 ** -8 * (out[0].double().abs() @ Wh.abs().t())).all()
     # the stored experts are those of the layer's own dequantisation, up to its rounding to bf16
     assert ((q.qlora_nf4_dequant(gate).double() - dense(gate)).abs() <= 1.01 * 2.0 ** -8 * dense(gate).abs()).all()
+
+
+def test_outputs_of_another_stream_are_not_reused():
+    # torch allocates the outputs on the current stream; dropped while the other stream still writes them, their
+    # blocks must not be handed out again
+    T, d, f, E, k = 5, 768, 256, 4, 2
+    a = layer(T, d, f, E, seed=15)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    out = q.qlora_moe_fwd(*a, k, stream=s)
+    used = {t.data_ptr() for t in out}
+    del out
+    fresh = [torch.empty(T, d, dtype=torch.bfloat16, device="cuda"), torch.empty(T, k, device="cuda"),
+             torch.empty(T, k, device="cuda")]
+    assert not used & {t.data_ptr() for t in fresh}
+    s.synchronize()
