@@ -492,8 +492,7 @@ cudaError_t f4_launch(const F4Args &a, int64_t groups, cudaStream_t st) {
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = CLUSTER ? at : at + 1;
-    static std::atomic<uint64_t> ready{0};
-    cudaError_t e = set_smem_once(kernel, smem, ready);
+    cudaError_t e = set_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     // clusters that run at once: fewer than SMs / size where the chip's SM groups do not divide
     int most = num_sms();

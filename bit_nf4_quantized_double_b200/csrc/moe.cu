@@ -37,6 +37,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "launch.h"
 #include "tc.cuh"
@@ -1125,8 +1126,7 @@ cudaError_t launch_moe(const __nv_bfloat16 *X, int64_t T, const void *router, bo
     const Codebook &cb = host_codebook();
     for (int i = 0; i < 16; ++i) a.q[i] = cb.q[i];
     const int sms = num_sms();
-    static std::atomic<uint64_t> ready{0};
-    cudaError_t e = set_smem_once(k_moe_experts, kMoeSmem, ready);
+    cudaError_t e = set_smem(k_moe_experts, kMoeSmem);
     if (e != cudaSuccess) return e;
     static std::atomic<bool> window{false};                  // the kernel's shared addresses are absolute
     if (!window.load(std::memory_order_relaxed)) {

@@ -4,7 +4,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <atomic>
 #include <mutex>
 #include <utility>
 
@@ -82,18 +81,6 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int block, siz
 template <typename K>
 inline cudaError_t set_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-// set_smem once per device for one kernel; `done` is that kernel's own (a bit per device).
-template <typename K>
-inline cudaError_t set_smem_once(K kernel, int bytes, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-    if ((e = set_smem(kernel, bytes)) == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
 }
 
 }  // namespace qnf4
