@@ -998,7 +998,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) k_moe_experts(const __grid_con
 
     // ---------------- Y[t] = sum over choices in order, each the sum of its chunks in order
     const int d4 = a.D / 4, parts = a.k * a.nck2;
-    for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < a.T * d4; i += (int)gridDim.x * kMoeThreads) {
+    // (eight lanes read a line of 128 bytes; the lines are dealt out over the CTAs)
+    for (int i = (int)((threadIdx.x >> 3) * gridDim.x + blockIdx.x) * 8 + (threadIdx.x & 7); i < a.T * d4;
+         i += (int)gridDim.x * kMoeThreads) {
         const int t = i / d4, d = i - t * d4;
         const float4 *src = reinterpret_cast<const float4 *>(a.part + (int64_t)t * parts * a.D) + d;
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
