@@ -26,8 +26,8 @@
 // them tokens: what the roles share (shares of the phases, lists) stays in shared memory, since
 // every spill in the products costs (147 instead of 127 us for the second case below).
 //
-// Measured, (T, E, k, d, f): (1, 8, 2, 4096, 11008) 52 us, (4, ...) 121, (32, ...) 214, floors of
-// 21 / 58 / 85 at the measured copy rate; (1, 64, 8, 2048, 1024) 25 us, (16, ...) 70. About 16 us
+// Measured, (T, E, k, d, f): (1, 8, 2, 4096, 11008) 52 us, (4, ...) 120, (32, ...) 211, floors of
+// 21 / 58 / 85 at the measured copy rate; (1, 64, 8, 2048, 1024) 25 us, (16, ...) 69. About 16 us
 // are fixed: logits, choice (2.5 to 5.5), two grid barriers (1.2 each), first copies, last sums. A
 // group of 16 warps' tiles, 32 KB, takes 1.0 us (0.74 at the copy rate).
 //
