@@ -197,3 +197,24 @@ def test_output_of_another_stream_is_not_reused():
     fresh = torch.empty(M, rows, dtype=torch.bfloat16, device="cuda")
     assert fresh.data_ptr() != used
     s.synchronize()
+
+
+# clusters with more tiles than a segment holds, an odd number of them, and a last tile of four rows
+@pytest.mark.parametrize("M,rows,cols", [(2, 38500, 4352), (10, 19508, 4352), (1, 38500, 4160)])
+def test_several_segments(M, rows, cols):
+    X, codes, absmax = inputs(M, rows, cols, seed=M)
+    Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, "fp4_e2m1", out_dtype=torch.float32)
+    check(Y, X, codes, absmax, rows, "fp4_e2m1")
+
+
+def test_timed_launches_give_the_same():
+    # the profiling hooks launch without the overlap of neighbouring kernels
+    X, codes, absmax = inputs(4, 300, 4096, seed=23)
+    first = q.qlora_fmt4_linear_fwd(X, codes, absmax, 300, "int4")
+    q.qlora_profile_enable(True)
+    try:
+        timed = q.qlora_fmt4_linear_fwd(X, codes, absmax, 300, "int4")
+        torch.cuda.synchronize()
+    finally:
+        q.qlora_profile_enable(False)
+    assert torch.equal(first, timed)

@@ -225,3 +225,24 @@ def test_outputs_of_another_stream_are_not_reused():
              torch.empty(T, k, device="cuda")]
     assert not used & {t.data_ptr() for t in fresh}
     s.synchronize()
+
+
+# the widest layer either way (16 chunks of D, of F), every token at one expert (eight full jobs), all of two
+@pytest.mark.parametrize("T,d,f,E,k", [(1, 65536, 64, 2, 1), (3, 64, 65536, 1, 1), (64, 128, 128, 1, 1), (64, 256, 64, 2, 2)])
+def test_extremes(T, d, f, E, k):
+    a = layer(T, d, f, E, seed=T + E)
+    check(q.qlora_moe_fwd(*a, k), reference(*a, k, True))
+
+
+def test_timed_launches_give_the_same():
+    # the profiling hooks launch without the overlap of neighbouring kernels
+    a = layer(5, 512, 320, 8, seed=19)
+    first = q.qlora_moe_fwd(*a, 3)
+    q.qlora_profile_enable(True)
+    try:
+        timed = q.qlora_moe_fwd(*a, 3)
+        torch.cuda.synchronize()
+    finally:
+        q.qlora_profile_enable(False)
+    assert all(torch.equal(x, y) for x, y in zip(first, timed))
+    check(timed, reference(*a, 3, True))
