@@ -246,3 +246,34 @@ def test_timed_launches_give_the_same():
         q.qlora_profile_enable(False)
     assert all(torch.equal(x, y) for x, y in zip(first, timed))
     check(timed, reference(*a, 3, True))
+
+
+def test_two_graphs_and_a_product_at_once():
+    # replays on two streams, each with its own workspace, and the 4-bit product on a third: a layer that waits for its
+    # CTAs shares the chip with the others
+    T, d, f, E, k = 8, 1024, 512, 16, 4
+    a = layer(T, d, f, E, seed=25)
+    first = q.qlora_moe_fwd(*a, k)
+    W = torch.randn(4096, d, device="cuda") * 0.02
+    codes, absmax = q.qlora_fmt4_quantize(W, "int4")
+    Y = q.qlora_fmt4_linear_fwd(a[0], codes, absmax, 4096, "int4")
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        ws = torch.empty(q.qlora_moe_fwd_workspace(T, d, f, E, k), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = [q.qlora_moe_fwd(*a, k, ws=ws) for _ in range(4)]
+        graphs.append((g, outs, ws, torch.cuda.Stream()))
+    third = torch.cuda.Stream()
+    products = []
+    for _ in range(5):
+        for g, _, _, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(third):
+            products += [q.qlora_fmt4_linear_fwd(a[0], codes, absmax, 4096, "int4") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert q.qlora_get_device_status() == q.QLORA_OK
+    assert all(torch.equal(x, y) for _, outs, _, _ in graphs for o in outs for x, y in zip(first, o))
+    assert all(torch.equal(Y, p) for p in products)
