@@ -16,7 +16,9 @@
 // multiplications by powers of two that the compiler does not know, which run on the other
 // integer pipe. Bits further down would need fewer shifts, but the sum inside mma aligns its
 // terms by their exponent fields, so that a small subnormal costs the others low bits
-// (measured 2e-6 instead of 1e-7 of the result).
+// (measured 2e-6 instead of 1e-7 of the result). For up to eight tokens Int4 takes a byte from a
+// table instead, a word per lane: one permute, one multiplication on the other pipe and one load
+// per two codes. All of a word's codes: 33.7 us for [28672, 8192], half of them 33.9, none 35.8.
 //
 // Tokens become fp16 after scaling by 2^-e, set per token and 256 inputs so that the largest
 // lies in [2^14, 2^15): exact for every bf16 within 2^-31 of the largest of its 256
@@ -35,8 +37,8 @@
 // memory and a whole row per warp need no sums, but a warp per tile is 12 warps per SM at
 // [28672, 8192], too few to hide the latencies of the products.)
 //
-// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.5 / 35.5 us for E2M1 / E3M0 / Int4 (75 /
-// 64 / 57 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
+// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.4 / 33.7 us for E2M1 / E3M0 / Int4 (75 /
+// 64 / 60 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
 // weight, which is launch, first latencies and one sum. E2M1 with 8 tokens 28.3 us, with 9 to 16
 // tokens 43 to 44: two operand sets of 32 registers, twice the matrix instructions.
 #include <algorithm>
@@ -73,8 +75,15 @@ __host__ __device__ constexpr int f4_buf_bytes(int nt) { return kF4Round * kF4Wa
 __host__ __device__ constexpr int f4_bar_at(int nt) { return kF4SumAt + 2 * f4_buf_bytes(nt); }
 __host__ __device__ constexpr int f4_seg_at(int nt) { return f4_bar_at(nt) + kF4Warps * 16 + 32; }
 __host__ __device__ constexpr int f4_seg_tiles(int nt) { return 32 / nt; }
-constexpr int f4_smem(int nt, bool cluster) { return 1024 + f4_seg_at(nt) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0); }
-static_assert(f4_smem(1, true) <= 232448 && f4_smem(2, true) <= 232448, "shared memory");
+// the lookup table, if there is one: 256 bytes of codes, a word for each lane
+constexpr int kF4TableBytes = 256 * 128;
+__host__ __device__ constexpr int f4_table_at(int nt, bool cluster) {
+    return (f4_seg_at(nt) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0) + 127) / 128 * 128;
+}
+constexpr int f4_smem(int nt, bool cluster, bool table) {
+    return 1024 + f4_table_at(nt, cluster) + (table ? kF4TableBytes : 0);
+}
+static_assert(f4_smem(1, true, true) <= 232448 && f4_smem(2, true, false) <= 232448, "shared memory");
 
 // A warp's sums of a tile are [token][row], permuted so that the 32 lanes of a store (eight even
 // or odd rows of tokens 2 t, or of tokens 2 t + 1) touch every bank once.
@@ -93,7 +102,7 @@ struct F4Args {
     int wk;                    // warps along a row in a CTA; the CTA's 16 / wk tiles lie side by side
     int nch, passes;           // CTAs along a row (cluster size); passes over a segment's rows
     int y_f32, vec_scales;
-    uint32_t two2, two4, two8, two12;   // 2^2, 2^4, 2^8, 2^12
+    uint32_t two2, two4, two7, two8, two12;   // 2^2, 2^4, 2^7, 2^8, 2^12
     float factor;              // (power of two of the decoded weights) / S
 };
 
@@ -129,6 +138,16 @@ __device__ __forceinline__ void decode(const F4Args &a, uint32_t w, uint32_t (&p
         p[3] = f16x2_of_e3m2((uint16_t)(hi >> 16));
     }
 }
+
+// Codes of a word by the table: a permute picks the byte, a multiplication on the other integer pipe makes the address.
+// Pairs as E2M1's: (1, 0) (3, 2) (5, 4) (7, 6). No one writes the table after it was filled: the loads may move freely.
+__device__ __forceinline__ void decode_table(const F4Args &a, uint32_t w, uint32_t table, uint32_t (&p)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("ld.shared.u32 %0, [%1];" : "=r"(p[i]) : "r"(prmt(w, 0u, 0x4440u | (uint32_t)i) * a.two7 + table));
+}
+// A code's value as the table holds it (Int4), in eighths.
+__device__ __forceinline__ float table_value(int c) { return (c & 8 ? -0.125f : 0.125f) * (float)(c & 7); }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -255,7 +274,7 @@ __device__ __forceinline__ void f4_store(const F4Args &a, int64_t m, int64_t row
     else static_cast<__nv_bfloat16 *>(a.Y)[m * a.N + row] = __float2bfloat16_rn(y);
 }
 
-template <int FMT, int NT, bool CLUSTER, bool VEC>
+template <int FMT, int NT, bool CLUSTER, bool VEC, bool TABLE>
 __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_constant__ F4Args a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int R = kF4Round, PIECE = f4_piece(NT), BUF = f4_buf_bytes(NT);
@@ -277,6 +296,12 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
         tma_prefetch_desc(&a.codes);
         if (VEC) tma_prefetch_desc(&a.scales);
     }
+    const uint32_t table = smem_addr(smem) + f4_table_at(NT, CLUSTER) + lane * 4;
+    if (TABLE)
+        for (int i = threadIdx.x; i < 256 * 8; i += kF4Threads) {
+            const uint32_t v = f16x2_of(table_value((i >> 3) & 15), table_value(i >> 7));
+            *reinterpret_cast<uint4 *>(smem + f4_table_at(NT, CLUSTER) + i * 16) = make_uint4(v, v, v, v);
+        }
     __syncthreads();
     // A kernel behind this one may be set up while this one runs; both touch global memory only after
     // the kernel before them has ended.
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                     };
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        f4_tokens<FMT>(a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * kF4StepK, lane, stage, xb[nt],
+                        f4_tokens<TABLE ? QLORA_FMT4_FP4_E2M1 : FMT>(a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * kF4StepK, lane, stage, xb[nt],
                                        up[nt][0], up[nt][1]);
                 }
             }
@@ -417,8 +442,13 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 uint32_t p[4], q[4];
-                                decode<FMT>(a, j ? u.y : u.x, p);
-                                decode<FMT>(a, j ? v.y : v.x, q);
+                                if (TABLE) {
+                                    decode_table(a, j ? u.y : u.x, table, p);
+                                    decode_table(a, j ? v.y : v.x, table, q);
+                                } else {
+                                    decode<FMT>(a, j ? u.y : u.x, p);
+                                    decode<FMT>(a, j ? v.y : v.x, q);
+                                }
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     const uint32_t *x = xb[nt] + 8 * b + 4 * j;
@@ -477,10 +507,10 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     }
 }
 
-template <int FMT, int NT, bool CLUSTER, bool VEC>
+template <int FMT, int NT, bool CLUSTER, bool VEC, bool TABLE>
 cudaError_t f4_launch(const F4Args &a, int64_t groups, cudaStream_t st) {
-    auto kernel = k_fmt4_linear<FMT, NT, CLUSTER, VEC>;
-    constexpr int smem = f4_smem(NT, CLUSTER);
+    auto kernel = k_fmt4_linear<FMT, NT, CLUSTER, VEC, TABLE>;
+    constexpr int smem = f4_smem(NT, CLUSTER, TABLE);
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -513,16 +543,24 @@ cudaError_t f4_launch(const F4Args &a, int64_t groups, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, bool TABLE>
 cudaError_t f4_launch_form(const F4Args &a, int64_t groups, cudaStream_t st) {
     if (a.nch > 1 || a.passes > 1)
-        return a.vec_scales ? f4_launch<FMT, NT, true, true>(a, groups, st) : f4_launch<FMT, NT, true, false>(a, groups, st);
-    return a.vec_scales ? f4_launch<FMT, NT, false, true>(a, groups, st) : f4_launch<FMT, NT, false, false>(a, groups, st);
+        return a.vec_scales ? f4_launch<FMT, NT, true, true, TABLE>(a, groups, st) : f4_launch<FMT, NT, true, false, TABLE>(a, groups, st);
+    return a.vec_scales ? f4_launch<FMT, NT, false, true, TABLE>(a, groups, st) : f4_launch<FMT, NT, false, false, TABLE>(a, groups, st);
 }
 
 template <int FMT>
-cudaError_t f4_launch_tiles(const F4Args &a, int64_t groups, cudaStream_t st) {
-    return a.M <= 8 ? f4_launch_form<FMT, 1>(a, groups, st) : f4_launch_form<FMT, 2>(a, groups, st);
+cudaError_t f4_launch_tiles(F4Args &a, int64_t groups, cudaStream_t st) {
+    if (a.M > 8) return f4_launch_form<FMT, 2, false>(a, groups, st);
+    // The table pays for Int4 once every CTA has work: [28672, 8192] 33.7 us instead of 35.8, [4096, 4096] 5.6 instead of 5.8,
+    // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it), and E3M0 34.0 instead of 31.3. Beside the sums of
+    // 16 tokens there is no room for it.
+    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms()) {
+        a.factor = 8.0f / 7.0f;
+        return f4_launch_form<FMT, 1, FMT == QLORA_FMT4_INT4>(a, groups, st);
+    }
+    return f4_launch_form<FMT, 1, false>(a, groups, st);
 }
 
 }  // namespace
@@ -545,6 +583,7 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
     a.y_f32 = y_f32;
     a.two2 = 4;
     a.two4 = 16;
+    a.two7 = 128;
     a.two8 = 256;
     a.two12 = 4096;
     a.vec_scales = a.kbs % 4 == 0 && aligned16(absmax);

@@ -218,3 +218,17 @@ def test_timed_launches_give_the_same():
     finally:
         q.qlora_profile_enable(False)
     assert torch.equal(first, timed)
+
+
+# Int4 with work for every CTA, which takes the codes from a table: one CTA or a cluster along the row, constants that do
+# or do not start on 16 bytes, tiles side by side
+@pytest.mark.parametrize("M,rows,cols", [(1, 2400, 4096), (8, 2500, 4032), (3, 1300, 4160), (5, 1250, 8192), (2, 20011, 1024)])
+def test_int4_table(M, rows, cols):
+    X, codes, absmax = inputs(M, rows, cols, seed=M + rows)
+    Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, "int4", out_dtype=torch.float32)
+    check(Y, X, codes, absmax, rows, "int4")
+    # one input after the other: every code of a row by itself, and its constant's sign
+    X1 = torch.zeros(M, cols, dtype=torch.bfloat16, device="cuda")
+    X1[:, 7] = 1e30
+    X1[:, cols - 3] = -1e-30
+    check(q.qlora_fmt4_linear_fwd(X1, codes, -absmax, rows, "int4", out_dtype=torch.float32), X1, codes, -absmax, rows, "int4")
