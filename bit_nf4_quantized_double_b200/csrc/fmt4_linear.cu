@@ -17,8 +17,9 @@
 // integer pipe. Bits further down would need fewer shifts, but the sum inside mma aligns its
 // terms by their exponent fields, so that a small subnormal costs the others low bits
 // (measured 2e-6 instead of 1e-7 of the result). For up to eight tokens Int4 takes a byte from a
-// table instead, a word per lane: one permute, one multiplication on the other pipe and one load
-// per two codes. All of a word's codes: 33.7 us for [28672, 8192], half of them 33.9, none 35.8.
+// table instead, a word per lane: one permute, which is the address, and one load per two codes
+// (32.1 us for [28672, 8192], without a table 35.8; with rows of 128 bytes, whose addresses take
+// a multiplication more, 33.7, and half of the codes by those 33.9).
 //
 // Tokens become fp16 after scaling by 2^-e, set per token and 256 inputs so that the largest
 // lies in [2^14, 2^15): exact for every bf16 within 2^-31 of the largest of its 256
@@ -37,8 +38,8 @@
 // memory and a whole row per warp need no sums, but a warp per tile is 12 warps per SM at
 // [28672, 8192], too few to hide the latencies of the products.)
 //
-// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.4 / 33.7 us for E2M1 / E3M0 / Int4 (75 /
-// 64 / 60 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
+// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.4 / 32.1 us for E2M1 / E3M0 / Int4 (75 /
+// 64 / 63 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
 // weight, which is launch, first latencies and one sum. E2M1 with 8 tokens 28.3 us, with 9 to 16
 // tokens 43 to 44: two operand sets of 32 registers, twice the matrix instructions.
 #include <algorithm>
@@ -72,17 +73,16 @@ constexpr int kF4ScaleAt = kF4Warps * kF4Stages * kF4StageBytes;
 constexpr int kF4SumAt = kF4ScaleAt + kF4Warps * kF4Stages * kF4ScaleBytes;
 __host__ __device__ constexpr int f4_piece(int nt) { return 16 * 8 * nt * 4; }          // a warp's sums of a tile
 __host__ __device__ constexpr int f4_buf_bytes(int nt) { return kF4Round * kF4Warps * f4_piece(nt); }
-__host__ __device__ constexpr int f4_bar_at(int nt) { return kF4SumAt + 2 * f4_buf_bytes(nt); }
-__host__ __device__ constexpr int f4_seg_at(int nt) { return f4_bar_at(nt) + kF4Warps * 16 + 32; }
+// With a lookup table (a word per byte of codes and lane) its 256 rows are 256 bytes apart, so that a permute of a byte
+// and the lane makes an address; the other halves of the rows hold the sums.
+__host__ __device__ constexpr int f4_bar_at(int nt, bool table) { return kF4SumAt + (table ? 65536 : 2 * f4_buf_bytes(nt)); }
+__host__ __device__ constexpr int f4_seg_at(int nt, bool table) { return f4_bar_at(nt, table) + kF4Warps * 16 + 32; }
 __host__ __device__ constexpr int f4_seg_tiles(int nt) { return 32 / nt; }
-// the lookup table, if there is one: 256 bytes of codes, a word for each lane
-constexpr int kF4TableBytes = 256 * 128;
-__host__ __device__ constexpr int f4_table_at(int nt, bool cluster) {
-    return (f4_seg_at(nt) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0) + 127) / 128 * 128;
-}
 constexpr int f4_smem(int nt, bool cluster, bool table) {
-    return 1024 + f4_table_at(nt, cluster) + (table ? kF4TableBytes : 0);
+    return 1024 + f4_seg_at(nt, table) + (cluster ? f4_seg_tiles(nt) * f4_piece(nt) : 0);
 }
+static_assert(2 * f4_buf_bytes(1) <= 256 * 128, "the sums between the table's rows");
+constexpr int kF4Reserved = 1024;                                      // the window's first bytes, which the system keeps
 static_assert(f4_smem(1, true, true) <= 232448 && f4_smem(2, true, false) <= 232448, "shared memory");
 
 // A warp's sums of a tile are [token][row], permuted so that the 32 lanes of a store (eight even
@@ -102,7 +102,7 @@ struct F4Args {
     int wk;                    // warps along a row in a CTA; the CTA's 16 / wk tiles lie side by side
     int nch, passes;           // CTAs along a row (cluster size); passes over a segment's rows
     int y_f32, vec_scales;
-    uint32_t two2, two4, two7, two8, two12;   // 2^2, 2^4, 2^7, 2^8, 2^12
+    uint32_t two2, two4, two8, two12;   // 2^2, 2^4, 2^8, 2^12
     float factor;              // (power of two of the decoded weights) / S
 };
 
@@ -139,12 +139,14 @@ __device__ __forceinline__ void decode(const F4Args &a, uint32_t w, uint32_t (&p
     }
 }
 
-// Codes of a word by the table: a permute picks the byte, a multiplication on the other integer pipe makes the address.
-// Pairs as E2M1's: (1, 0) (3, 2) (5, 4) (7, 6). No one writes the table after it was filled: the loads may move freely.
-__device__ __forceinline__ void decode_table(const F4Args &a, uint32_t w, uint32_t table, uint32_t (&p)[4]) {
+// Codes of a word by the table. at: the lane's word of row 0, without the constant kF4Reserved + kF4SumAt; its upper half
+// holds the CTA's place in its cluster, its second byte is zero. Pairs as E2M1's: (1, 0) (3, 2) (5, 4) (7, 6). No one writes
+// the table after it was filled: the loads may move freely.
+__device__ __forceinline__ void decode_table(uint32_t w, uint32_t at, uint32_t (&p)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        asm("ld.shared.u32 %0, [%1];" : "=r"(p[i]) : "r"(prmt(w, 0u, 0x4440u | (uint32_t)i) * a.two7 + table));
+        asm("ld.shared.u32 %0, [%1 + %2];"
+            : "=r"(p[i]) : "r"(prmt(w, at, 0x7604u | ((uint32_t)i << 4))), "n"(kF4Reserved + kF4SumAt));
 }
 // A code's value as the table holds it (Int4), in eighths.
 __device__ __forceinline__ float table_value(int c) { return (c & 8 ? -0.125f : 0.125f) * (float)(c & 7); }
@@ -277,15 +279,22 @@ __device__ __forceinline__ void f4_store(const F4Args &a, int64_t m, int64_t row
 template <int FMT, int NT, bool CLUSTER, bool VEC, bool TABLE>
 __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_constant__ F4Args a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int R = kF4Round, PIECE = f4_piece(NT), BUF = f4_buf_bytes(NT);
+    constexpr int R = kF4Round, SPREAD = TABLE ? 2 : 1, PIECE = SPREAD * f4_piece(NT), BUF = SPREAD * f4_buf_bytes(NT);
+    // offset of byte o of a warp's sums
+    auto spread = [](int o) { return TABLE ? 2 * (o & ~127) + 128 + (o & 127) : o; };
     uint8_t *smem = align1024(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * (kF4Stages * kF4StageBytes);
     const uint32_t cring = smem_addr(smem) + kF4ScaleAt + warp * (kF4Stages * kF4ScaleBytes);
-    const uint32_t full = smem_addr(smem) + f4_bar_at(NT) + warp * 16;               // the ring's two rounds
-    const uint32_t bar = smem_addr(smem) + f4_bar_at(NT) + kF4Warps * 16;   // a round's sums are written
-    volatile int *abort = reinterpret_cast<int *>(smem + f4_bar_at(NT) + kF4Warps * 16 + 8);
-    float *seg = reinterpret_cast<float *>(smem + f4_seg_at(NT));
+    const uint32_t full = smem_addr(smem) + f4_bar_at(NT, TABLE) + warp * 16;               // the ring's two rounds
+    const uint32_t bar = smem_addr(smem) + f4_bar_at(NT, TABLE) + kF4Warps * 16;   // a round's sums are written
+    volatile int *abort = reinterpret_cast<int *>(smem + f4_bar_at(NT, TABLE) + kF4Warps * 16 + 8);
+    float *seg = reinterpret_cast<float *>(smem + f4_seg_at(NT, TABLE));
+    // the table's address is made of constants: the window's start below the cluster place has to be the expected one
+    if (TABLE && (smem_addr(smem) & 0xffffffu) != (uint32_t)kF4Reserved) {
+        if (threadIdx.x == 0) raise_status(QLORA_ERR_CUDA);
+        return;
+    }
     if (lane < 2) mbar_init(full + 8 * lane, 1);
     if (threadIdx.x == 0) {
         mbar_init(bar, kF4Warps);
@@ -296,11 +305,11 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
         tma_prefetch_desc(&a.codes);
         if (VEC) tma_prefetch_desc(&a.scales);
     }
-    const uint32_t table = smem_addr(smem) + f4_table_at(NT, CLUSTER) + lane * 4;
+    const uint32_t table = smem_addr(smem) - kF4Reserved + lane * 4;
     if (TABLE)
         for (int i = threadIdx.x; i < 256 * 8; i += kF4Threads) {
             const uint32_t v = f16x2_of(table_value((i >> 3) & 15), table_value(i >> 7));
-            *reinterpret_cast<uint4 *>(smem + f4_table_at(NT, CLUSTER) + i * 16) = make_uint4(v, v, v, v);
+            *reinterpret_cast<uint4 *>(smem + kF4SumAt + (i >> 3) * 256 + (i & 7) * 16) = make_uint4(v, v, v, v);
         }
     __syncthreads();
     // A kernel behind this one may be set up while this one runs; both touch global memory only after
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     // pieces of a buffer: [tiles side by side][tile of the round][warp along the row]
     const int mypiece = kF4SumAt + (tw * R * wk + kw) * PIECE;
     // this lane's place of token 2 t, row 2 g; the other token flips bit 6, the other row bit 5
-    const int put = 4 * f4_sum_at(2 * t, 2 * g);
+    const int put = spread(4 * f4_sum_at(2 * t, 2 * g));
 
     // Adds round `round` (tile groups i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
     // `act` warps that have a slice, in warp order.
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
             const int ti = e / (128 * NT), o = e & (128 * NT - 1), m = o >> 4, r = o & 15;
             const int i = ti & (R - 1);                     // ti = (tile side by side) * R + (tile of the round)
             if (i >= rn || m >= mn) continue;
-            const uint8_t *src = buf + ti * wk * PIECE + 4 * f4_sum_at(m, r);
+            const uint8_t *src = buf + ti * wk * PIECE + spread(4 * f4_sum_at(m, r));
             float y = 0.0f;
             if (act == kF4Warps) {
                 float v[kF4Warps];
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                     }
                     // handed over in the places of this warp's own sums (a pass before has been added)
                     auto stage = [&](int m, int u) {
-                        return reinterpret_cast<uint4 *>(smem + mypiece + (m >> 1) * BUF + (m & 1) * (wk * PIECE) + 16 * u);
+                        return reinterpret_cast<uint4 *>(smem + mypiece + (m >> 1) * BUF + (m & 1) * (wk * PIECE) + spread(16 * u));
                     };
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -443,8 +452,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                             for (int j = 0; j < 2; ++j) {
                                 uint32_t p[4], q[4];
                                 if (TABLE) {
-                                    decode_table(a, j ? u.y : u.x, table, p);
-                                    decode_table(a, j ? v.y : v.x, table, q);
+                                    decode_table(j ? u.y : u.x, table, p);
+                                    decode_table(j ? v.y : v.x, table, q);
                                 } else {
                                     decode<FMT>(a, j ? u.y : u.x, p);
                                     decode<FMT>(a, j ? v.y : v.x, q);
@@ -550,13 +559,28 @@ cudaError_t f4_launch_form(const F4Args &a, int64_t groups, cudaStream_t st) {
     return a.vec_scales ? f4_launch<FMT, NT, false, true, TABLE>(a, groups, st) : f4_launch<FMT, NT, false, false, TABLE>(a, groups, st);
 }
 
+// The table's address is absolute: dynamic shared memory has to start where it is expected.
+bool f4_window_ok() {
+    static std::atomic<int> known{0};
+    int k = known.load(std::memory_order_relaxed);
+    if (k == 0) {
+        int reserved = 0, dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
+            return false;
+        k = reserved == kF4Reserved ? 1 : -1;
+        known.store(k, std::memory_order_relaxed);
+    }
+    return k > 0;
+}
+
 template <int FMT>
 cudaError_t f4_launch_tiles(F4Args &a, int64_t groups, cudaStream_t st) {
     if (a.M > 8) return f4_launch_form<FMT, 2, false>(a, groups, st);
-    // The table pays for Int4 once every CTA has work: [28672, 8192] 33.7 us instead of 35.8, [4096, 4096] 5.6 instead of 5.8,
-    // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it), and E3M0 34.0 instead of 31.3. Beside the sums of
-    // 16 tokens there is no room for it.
-    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms()) {
+    // The table pays for Int4 once every CTA has work: [28672, 8192] 32.1 us instead of 35.8, [4096, 4096] 5.5 instead of 5.8,
+    // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it). E3M0 takes 31.4 without one. Beside the sums of 16
+    // tokens there is no room for it.
+    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && f4_window_ok()) {
         a.factor = 8.0f / 7.0f;
         return f4_launch_form<FMT, 1, FMT == QLORA_FMT4_INT4>(a, groups, st);
     }
@@ -583,7 +607,6 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
     a.y_f32 = y_f32;
     a.two2 = 4;
     a.two4 = 16;
-    a.two7 = 128;
     a.two8 = 256;
     a.two12 = 4096;
     a.vec_scales = a.kbs % 4 == 0 && aligned16(absmax);
