@@ -92,6 +92,7 @@ _SIGS = {
     "qlora_nf4_quantize_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(_Tensor),
                                                   ctypes.c_void_p]),
     "qlora_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_void_p]),
+    "qlora_selftest_wait_warp": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_selftest_rcp_error": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_nf4_merge_workspace": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
     "qlora_nf4_merge_adapter": (ctypes.c_int, [ctypes.POINTER(_Tensor), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,

@@ -253,14 +253,6 @@ __device__ __forceinline__ void f4_scales(const F4Args &a, uint32_t dst, int64_t
     }
 }
 
-// A bounded wait whose loop is out of line.
-__device__ __noinline__ bool f4_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return mbar_wait(bar, parity, abort);
-}
-__device__ __forceinline__ bool f4_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return mbar_try_wait(bar, parity) || f4_wait_slow(bar, parity, abort);
-}
-
 // Before an early exit: waits, within a limit, for the copies of rounds `used` .. `filled` - 1.
 __device__ __noinline__ void f4_drain(uint32_t full, uint32_t used, uint32_t filled) {
     cp_wait<0>();
@@ -344,7 +336,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     // Adds round `round` (tile groups i0 .. of this CTA, `rn` of them, the first at place sg of the segment) over the
     // `act` warps that have a slice, in warp order.
     auto add_round = [&](int round, int i0, int sg, int rn, int act, bool fresh) {
-        if (!f4_wait(bar, round & 1, abort)) return;
+        if (!mbar_wait_warp(bar, round & 1, abort)) return;
         const uint8_t *buf = smem + kF4SumAt + (round & 1) * BUF;
         for (int e = threadIdx.x; e < tg * R * 128 * NT; e += kF4Threads) {
             const int ti = e / (128 * NT), o = e & (128 * NT - 1), m = o >> 4, r = o & 15;
@@ -426,7 +418,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                     cp_wait<1>();
                     if (!VEC) __syncwarp();
                     const int h = (int)(used & 1u);
-                    const bool landed = f4_wait(full + 8 * h, (used >> 1) & 1u, abort);
+                    const bool landed = mbar_wait_warp(full + 8 * h, (used >> 1) & 1u, abort);
                     if (!landed) {
                         f4_drain(full, used, filled);         // the CTA goes on without this warp's slices
                         dead = true;

@@ -128,12 +128,6 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __noinline__ bool moe_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return mbar_wait(bar, parity, abort);
-}
-__device__ __forceinline__ bool moe_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return mbar_try_wait(bar, parity) || moe_wait_slow(bar, parity, abort);
-}
 
 // Eight values as fp16 after scaling by 2^-e, with 2^e such that the largest magnitude of the warp's
 // 256 lies in [2^14, 2^15); returns 2^e. NaN and infinity stay what they are.
@@ -555,7 +549,7 @@ __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, 
 #pragma unroll 1
     for (int phase = 0; phase < 2; ++phase) {
         const MoePhase &p = phase ? p1 : p0;
-        if (phase == 1 && p.count > 0 && !moe_wait(c.go, 0, c.abort)) return;   // every CTA's hidden values
+        if (phase == 1 && p.count > 0 && !mbar_wait_warp(c.go, 0, c.abort)) return;   // every CTA's hidden values
         int jobno = p.job, chunk = p.chunk, run = min(p.count, p.per - p.group);
 #pragma unroll 1
         for (int left = p.count; left > 0; left -= run, run = min(left, p.per)) {
@@ -569,7 +563,7 @@ __device__ __forceinline__ void moe_multiply(const MoeArgs &a, const MoeCta &c, 
 #pragma unroll 1
             for (const int end = n + run; n < end; ++n) {
                 const int st = n & (kMoeStages - 1);
-                if (!moe_wait(c.full + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
+                if (!mbar_wait_warp(c.full + 8 * st, (n / kMoeStages) & 1, c.abort)) return;
                 if (mine) {
                     const uint32_t lo = stage_at(st) + lo_at + at;
                     const uint8_t *scale = c.window + (sc + st * kMoeScaleBytes);
@@ -819,7 +813,7 @@ __device__ __forceinline__ void moe_copier(const MoeArgs &a, const MoeCta &c, co
 #pragma unroll 1
     for (int n = 0; n < total; ++n) {
         const int st = n & (kMoeStages - 1);
-        if (n >= kMoeStages && !moe_wait(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return;
+        if (n >= kMoeStages && !mbar_wait_warp(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return;
         moe_copy(a, c, cur.phase ? p1 : p0, cur, st);
         cur.next(p0, p1, c.jobs);
     }
@@ -847,7 +841,7 @@ __device__ __forceinline__ void moe_adder(const MoeArgs &a, const MoeCta &c, con
     for (int n = 0; n < total; ++n) {
         const int st = n & (kMoeStages - 1);
         if (turn == h) {
-            if (!moe_wait(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) {
+            if (!mbar_wait_warp(c.done + 8 * st, (n / kMoeStages) & 1, c.abort)) {
                 if (n < p0.count) meet();
                 return;
             }
@@ -879,7 +873,7 @@ __device__ __forceinline__ void moe_scaler(const MoeArgs &a, const MoeCta &c, co
     };
     auto step = [&](int n, MoeUnit &u, MoeRaw &r) {
         const int st = n & (kMoeStages - 1), phase = n >= p0.count;
-        if (n >= kMoeStages && !moe_wait(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return false;
+        if (n >= kMoeStages && !mbar_wait_warp(c.done + 8 * st, (n / kMoeStages - 1) & 1, c.abort)) return false;
         const float mu0 = phase ? mu[2] : mu[0], mu1 = phase ? mu[2] : mu[1];
         if ((phase ? p1 : p0).kbs & 3) moe_constants<false>(c, st, u, r, mu0, mu1);
         else moe_constants<true>(c, st, u, r, mu0, mu1);

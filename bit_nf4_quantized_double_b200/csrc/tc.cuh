@@ -72,9 +72,10 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
     return ok != 0;
 }
 // Wait for the phase of the given parity to complete. Gives up (returns
-// false, sets *abort and the device status) after kWaitLimitNs, or as soon
+// false, sets *abort and the device status) after limit_ns, or as soon
 // as another role of the CTA has given up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                          uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
@@ -82,12 +83,25 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
         if (*abort) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             *abort = 1;
             raise_status(QLORA_ERR_TIMEOUT);
             return false;
         }
     }
+}
+// mbar_wait by all 32 lanes of a converged warp, with one answer for the warp. A lane that reads the
+// abort flag or the clock just before the phase completes would give up alone, and the others would
+// wait for it without a limit in their next shuffle, mma or __syncwarp: so one lane that gave up
+// is enough for all. The loop is out of line.
+[[maybe_unused]] static __device__ __noinline__ bool mbar_wait_warp_slow(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                                         uint64_t limit_ns) {
+    const bool ok = mbar_wait(bar, parity, abort, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort,
+                                               uint64_t limit_ns = kWaitLimitNs) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_warp_slow(bar, parity, abort, limit_ns);
 }
 __device__ __forceinline__ void fence_barrier_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

@@ -377,6 +377,18 @@ qlora_status qlora_nf4_merge_adapter(const qlora_nf4_tensor *W, const void *A, c
 qlora_status qlora_selftest_wait_timeout(qlora_stream_t stream);
 
 /*
+ * Self-test of the same wait made by all 32 lanes of a warp, which have to get one answer:
+ * a lane that gave up alone would leave the others waiting for it. Launches one kernel of
+ * 97 waits that end by completion, by the abort flag, by both at nearly the same time, and
+ * (the last) by a limit of 1 ms, which records QLORA_ERR_TIMEOUT in the status word. `out`,
+ * four device words, receives the waits whose lanes disagreed, those with a wrong answer
+ * (both have to be 0), those that gave up, and their number.
+ * Returns QLORA_ERR_INVALID_ARG for a NULL or misaligned pointer, QLORA_ERR_CUDA on a
+ * launch failure.
+ */
+qlora_status qlora_selftest_wait_warp(unsigned int *out, qlora_stream_t stream);
+
+/*
  * Self-test of the reciprocal approximation behind the quantiser's fast code search
  * (the page has no counterpart; the search is exact only while the approximation
  * stays within a few ulps). Measures |r - 1/m| over every fp32 mantissa m in [1, 2),
