@@ -43,7 +43,6 @@
 // weight, which is launch, first latencies and one sum. E2M1 with 8 tokens 28.3 us, with 9 to 16
 // tokens 43 to 44: two operand sets of 32 registers, twice the matrix instructions.
 #include <algorithm>
-#include <atomic>
 
 #include "launch.h"
 #include "tc.cuh"
@@ -285,6 +284,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
     // the table's address is made of constants: the window's start below the cluster place has to be the expected one
     if (TABLE && (smem_addr(smem) & 0xffffffu) != (uint32_t)kF4Reserved) {
         if (threadIdx.x == 0) raise_status(QLORA_ERR_CUDA);
+        griddep_wait();                                // the kernel before ends before this one
         return;
     }
     if (lane < 2) mbar_init(full + 8 * lane, 1);
@@ -528,15 +528,17 @@ cudaError_t f4_launch(const F4Args &a, int64_t groups, cudaStream_t st) {
     // clusters that run at once: fewer than SMs / size where the chip's SM groups do not divide
     int most = num_sms();
     if (CLUSTER) {
-        static std::atomic<int> active[kF4MaxCluster + 1];
-        most = active[a.nch].load(std::memory_order_relaxed);
-        if (most == 0) {
+        static DeviceCache active[kF4MaxCluster + 1];
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        most = active[a.nch].get(dev, [&] {
+            int n = 0;
             cfg.gridDim = dim3((unsigned)a.nch);
             cfg.numAttrs = 1;
-            if ((e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg)) != cudaSuccess) return e;
-            if (most < 1) most = 1;
-            active[a.nch].store(most, std::memory_order_relaxed);
-        }
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            return e == cudaSuccess ? std::max(n, 1) : 0;
+        });
+        if (e != cudaSuccess) return e;
     }
     cfg.numAttrs = (CLUSTER ? 1 : 0) + (profiling_launches() ? 0 : 1);
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(groups, most) * a.nch), (unsigned)ceil_div(a.M, (int64_t)kF4Tokens));
@@ -551,28 +553,13 @@ cudaError_t f4_launch_form(const F4Args &a, int64_t groups, cudaStream_t st) {
     return a.vec_scales ? f4_launch<FMT, NT, false, true, TABLE>(a, groups, st) : f4_launch<FMT, NT, false, false, TABLE>(a, groups, st);
 }
 
-// The table's address is absolute: dynamic shared memory has to start where it is expected.
-bool f4_window_ok() {
-    static std::atomic<int> known{0};
-    int k = known.load(std::memory_order_relaxed);
-    if (k == 0) {
-        int reserved = 0, dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev) != cudaSuccess)
-            return false;
-        k = reserved == kF4Reserved ? 1 : -1;
-        known.store(k, std::memory_order_relaxed);
-    }
-    return k > 0;
-}
-
 template <int FMT>
 cudaError_t f4_launch_tiles(F4Args &a, int64_t groups, cudaStream_t st) {
     if (a.M > 8) return f4_launch_form<FMT, 2, false>(a, groups, st);
     // The table pays for Int4 once every CTA has work: [28672, 8192] 32.1 us instead of 35.8, [4096, 4096] 5.5 instead of 5.8,
     // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it). E3M0 takes 31.4 without one. Beside the sums of 16
     // tokens there is no room for it.
-    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && f4_window_ok()) {
+    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && shared_window_at(kF4Reserved)) {
         a.factor = 8.0f / 7.0f;
         return f4_launch_form<FMT, 1, FMT == QLORA_FMT4_INT4>(a, groups, st);
     }

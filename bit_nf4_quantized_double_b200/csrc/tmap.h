@@ -1,6 +1,6 @@
 // Host helpers shared by the tcgen05 kernel files: TMA tensor-map encoding
-// (through the driver entry point, so the library needs no -lcuda) and the
-// dynamic shared-memory opt-in.
+// (through the driver entry point, so the library needs no -lcuda), the
+// dynamic shared-memory opt-in and where the shared window starts.
 #pragma once
 
 #include <cuda.h>
@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "device_cache.h"
 
 namespace qnf4 {
 
@@ -81,6 +82,18 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), int grid, int block, siz
 template <typename K>
 inline cudaError_t set_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Whether the current device keeps the first `low` bytes of the shared window for the system, so that
+// a kernel without static shared memory finds its dynamic shared memory at that address.
+inline bool shared_window_at(int low) {
+    static DeviceCache reserved;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    return reserved.get(dev, [&] {
+        int bytes = 0;
+        return cudaDeviceGetAttribute(&bytes, cudaDevAttrReservedSharedMemoryPerBlock, dev) == cudaSuccess ? bytes + 1 : 0;
+    }) == low + 1;
 }
 
 }  // namespace qnf4

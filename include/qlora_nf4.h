@@ -251,7 +251,9 @@ qlora_status qlora_linear_fwd_grouped(int64_t M, int count, const qlora_linear_d
  * token with a NaN or an infinity are what the formula gives for the experts chosen that way.
  * Two launches; the second is cooperative (one CTA per SM, two bounded grid barriers:
  * QLORA_ERR_TIMEOUT in the status word if one runs out). QLORA_ERR_CUDA where the device
- * cannot hold all its CTAs at once.
+ * cannot hold all its CTAs at once, or where its shared memory does not start at the address
+ * that the kernel expects (in the status word if only the kernel can tell; Y is then not
+ * written).
  */
 size_t qlora_moe_fwd_workspace(int64_t T, int64_t d, int64_t f, int64_t E, int k);
 qlora_status qlora_moe_fwd(const void *X, int64_t T, const void *router, qlora_dtype rdt, int64_t E,
