@@ -102,8 +102,18 @@ struct F4Args {
     int nch, passes;           // CTAs along a row (cluster size); passes over a segment's rows
     int y_f32, vec_scales;
     uint32_t two2, two4, two8, two12;   // 2^2, 2^4, 2^8, 2^12
-    float factor;              // (power of two of the decoded weights) / S
 };
+
+// A decoded operand times 2^scale is v(code) 2^j / S times `factor` below, with j such that the factor lies in [1, 2):
+// Int4 operands are m 2^-16 (m / 8 from the table), an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7). The power of
+// two goes into the tokens' 2^e, so that all sums hold Y / factor: neither do they overflow where Y does not, nor do they
+// lose more than a bit as subnormals where Y is none. (Applied at the end it made the sums 16 Y for E3M0.)
+__host__ __device__ constexpr int operand_scale(int fmt, bool table) {
+    return fmt == QLORA_FMT4_INT4 ? (table ? 0 : 13) : fmt == QLORA_FMT4_FP4_E2M1 ? -3 : -4;
+}
+__host__ __device__ constexpr float sum_factor(int fmt) {
+    return fmt == QLORA_FMT4_INT4 ? 8.0f / 7.0f : fmt == QLORA_FMT4_FP4_E2M1 ? 8.0f / 6.0f : 1.0f;
+}
 
 // Codes of a word as four fp16 pairs; pair_code names the codes of pair p (low half, high half).
 template <int FMT>
@@ -172,8 +182,8 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
 // holds token g, inputs 64 b + 16 t + 8 j + 0..7 in xb[8 b + 4 j + p], in the order of the
 // decoded pairs. Lane u converts inputs 8 u .. 8 u + 7 of every token, which are one such
 // group, and hands them over in shared memory (stage(m, u): 512 bytes for each of four tokens).
-// up0, up1: 2^e of the tokens of accumulator columns 2 t and 2 t + 1.
-template <int FMT, typename Stage>
+// up0, up1: 2^(e + SCALE) of the tokens of accumulator columns 2 t and 2 t + 1.
+template <int FMT, int SCALE, typename Stage>
 __device__ __forceinline__ void f4_tokens(const __nv_bfloat16 *X, int mn, int K, int k0, int lane, Stage stage,
                                           uint32_t (&xb)[32], float &up0, float &up1) {
     const int g = lane >> 2, t = lane & 3;
@@ -199,9 +209,9 @@ __device__ __forceinline__ void f4_tokens(const __nv_bfloat16 *X, int mn, int K,
             uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                     __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
             big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
-            // 2^e from the exponent field of the largest; both powers kept normal
+            // 2^e from the exponent field of the largest; all powers kept normal
             const int ex = min(max((int)(big >> 7), 24), 254);          // 254 also for NaN and infinity
-            const float down = __uint_as_float((uint32_t)(268 - ex) << 23), up = __uint_as_float((uint32_t)(ex - 14) << 23);
+            const float down = __uint_as_float((uint32_t)(268 - ex) << 23), up = __uint_as_float((uint32_t)(ex - 14 + SCALE) << 23);
             float f[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -261,8 +271,9 @@ __device__ __noinline__ void f4_drain(uint32_t full, uint32_t used, uint32_t fil
             if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
+template <int FMT>
 __device__ __forceinline__ void f4_store(const F4Args &a, int64_t m, int64_t row, float y) {
-    y *= a.factor;
+    y *= sum_factor(FMT);
     if (a.y_f32) static_cast<float *>(a.Y)[m * a.N + row] = y;
     else static_cast<__nv_bfloat16 *>(a.Y)[m * a.N + row] = __float2bfloat16_rn(y);
 }
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 *dst = fresh ? y : *dst + y;
             } else {
                 const int row = ((first + i0) * tg + (ti / R) * rn + i) * kF4StepRows + r;
-                if (row < (int)a.N) f4_store(a, m0 + m, row, y);
+                if (row < (int)a.N) f4_store<FMT>(a, m0 + m, row, y);
             }
         }
     };
@@ -407,8 +418,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                     };
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        f4_tokens<TABLE ? QLORA_FMT4_FP4_E2M1 : FMT>(a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * kF4StepK, lane, stage, xb[nt],
-                                       up[nt][0], up[nt][1]);
+                        f4_tokens<TABLE ? QLORA_FMT4_FP4_E2M1 : FMT, operand_scale(FMT, TABLE)>(
+                            a.X + (m0 + 8 * nt) * a.K, mn - 8 * nt, a.K, sl * kF4StepK, lane, stage, xb[nt], up[nt][0], up[nt][1]);
                 }
             }
             for (int i0 = s0; i0 < s1; i0 += R, ++round) {
@@ -501,7 +512,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) k_fmt4_linear(const __grid_cons
                 if (m >= mn || row >= a.N) continue;
                 float y = 0.0f;
                 for (int c = 0; c < nch; ++c) y += ld_cluster_f32(map_to_rank(base + 4 * e, c));
-                f4_store(a, m0 + m, row, y);
+                f4_store<FMT>(a, m0 + m, row, y);
             }
             cluster_sync();                            // before the next segment's sums, or the exit
         }
@@ -559,10 +570,8 @@ cudaError_t f4_launch_tiles(F4Args &a, int64_t groups, cudaStream_t st) {
     // The table pays for Int4 once every CTA has work: [28672, 8192] 32.1 us instead of 35.8, [4096, 4096] 5.5 instead of 5.8,
     // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it). E3M0 takes 31.4 without one. Beside the sums of 16
     // tokens there is no room for it.
-    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && shared_window_at(kF4Reserved)) {
-        a.factor = 8.0f / 7.0f;
+    if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && shared_window_at(kF4Reserved))
         return f4_launch_form<FMT, 1, FMT == QLORA_FMT4_INT4>(a, groups, st);
-    }
     return f4_launch_form<FMT, 1, false>(a, groups, st);
 }
 
@@ -589,8 +598,6 @@ cudaError_t launch_fmt4_linear(const __nv_bfloat16 *X, int64_t M, const uint8_t 
     a.two8 = 256;
     a.two12 = 4096;
     a.vec_scales = a.kbs % 4 == 0 && aligned16(absmax);
-    // Int4 operands are m 2^-16; an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7)
-    a.factor = f == QLORA_FMT4_INT4 ? 65536.0f / 7.0f : f == QLORA_FMT4_FP4_E2M1 ? 1.0f / 6.0f : 0.0625f;
     for (int one : {0, 1})
         if (a.vec_scales &&
             !make_map(one ? &a.scales_step : &a.scales, absmax, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)a.kbs, (uint64_t)rows,

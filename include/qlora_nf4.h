@@ -443,7 +443,9 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
  *   absmax  fp32 [rows, cols / 64], 4-byte aligned;
  *   Y       [M, rows], bf16 or fp32 by ydt, 16-byte aligned.
  * Every output is a sum in a fixed order. A NaN or infinity in X or absmax reaches the
- * outputs whose sums hold it, as in the formula. One kernel launch; no workspace.
+ * outputs whose sums hold it, as in the formula; the sums stay in fp32's range wherever Y's
+ * own do, for X of any size and absmax up to 2^100 (a block's sum meets its constant before
+ * the token's power of two). One kernel launch; no workspace.
  * QLORA_ERR_INVALID_ARG for a null or misaligned pointer, an unknown format or dtype;
  * QLORA_ERR_UNSUPPORTED_SHAPE for sizes outside the rules above (or rows above 2^30, cols
  * above 2^27).

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_double_b200 as q
+from oracle import formats as F
 
 pytestmark = pytest.mark.gpu
 
@@ -17,3 +18,33 @@ def test_a_warps_wait_has_one_answer():
     split, wrong, gave_up, waits = out.tolist()
     assert split == 0 and wrong == 0 and waits == 97
     assert 25 <= gave_up <= 73
+
+
+# Int4 takes its codes from a table for few tokens and many rows, by bit placement else
+@pytest.mark.parametrize("fmt", ["int4", "fp4_e2m1", "fp4_e3m0"])
+@pytest.mark.parametrize("M,rows", [(5, 40), (12, 40), (7, 4800)])
+@pytest.mark.parametrize("ec,ex", [(63, 64), (-60, -66), (99, 28), (-100, 60), (40, -166)])
+def test_ends_of_the_range(fmt, M, rows, ec, ex):
+    # one input per token, so that Y = v c x / S: results up to 3.2e38 and down to subnormals, far constants and far tokens.
+    # Roundings: the constant's product, the token's power of two (a half step if subnormal), 1 / S and its product; bf16's own
+    S, mags = F.FORMATS[fmt]
+    cols = 2048
+    g = torch.Generator(device="cuda").manual_seed(M + rows + ec)
+    X = torch.zeros(M, cols, dtype=torch.float64, device="cuda")
+    at = torch.randint(0, cols, (M,), generator=g, device="cuda")
+    sign = torch.randint(0, 2, (M,), generator=g, device="cuda").double() * 2 - 1
+    top = max(ex, -126)
+    X[torch.arange(M), at] = sign * 2.0 ** top
+    codes = torch.randint(0, 256, (rows * cols // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    absmax = (1 + 0.9 * torch.rand(rows * cols // 64, generator=g, device="cuda")) * 2.0 ** (ec + ex - top)
+    c = torch.stack((codes >> 4, codes & 15), 1).reshape(-1).long()
+    table = torch.tensor(mags + [-m for m in mags], dtype=torch.float64, device="cuda")
+    W = (table[c].view(-1, 64) * (absmax.double() / S)[:, None]).view(rows, cols)
+    ref = X @ W.t()
+    for dt in (torch.float32, torch.bfloat16):
+        Y = q.qlora_fmt4_linear_fwd(X.to(torch.bfloat16), codes, absmax, rows, fmt, out_dtype=dt).double()
+        tol = 2.0 ** -22 * ref.abs() + 2 * 2.0 ** -149
+        if dt == torch.bfloat16:
+            tol += 2.0 ** -8 * 1.001 * ref.abs() + 2.0 ** -134
+        assert torch.isfinite(Y).all() and ((Y - ref).abs() <= tol).all()
+    assert q.qlora_get_device_status() == q.QLORA_OK
