@@ -168,6 +168,15 @@ def _launch(what: str, fn, device: int, stream, *args):
         raise QloraError(status, what)
 
 
+def _dense(stream, *tensors):
+    """The tensors, those with strides as contiguous copies made on the call's stream: a caller can
+    order `stream` behind whatever wrote the tensors, but not behind a copy queued elsewhere."""
+    if all(t.is_contiguous() for t in tensors):
+        return tensors
+    with torch.cuda.stream(stream):                       # None: the current one
+        return tuple(t.contiguous() for t in tensors)
+
+
 def _hold(stream, *tensors):
     """Temporaries made for a call (contiguous copies, a workspace) are freed when the
     wrapper returns, while the kernels queued on `stream` may still read them. torch's
@@ -257,7 +266,7 @@ def qlora_nf4_quantize(W: torch.Tensor, out: NF4Tensor | None = None, ws: torch.
     need = int(L.qlora_nf4_quantize_workspace(rows, cols))
     wsb, wsn = _workspace(need, W.device, ws)
     t = out.ctype()
-    Wc = W.contiguous()
+    Wc, = _dense(stream, W)
     _check(L.qlora_nf4_quantize(_ptr(Wc), dt, ctypes.byref(t), _ptr(wsb), wsn, _stream(stream)),
            "qlora_nf4_quantize")
     _hold(stream, Wc, wsb)
@@ -275,7 +284,7 @@ def qlora_nf4_dequant(q: NF4Tensor, out: torch.Tensor | None = None, stream=None
 def qlora_nf4_quantize_grouped(Ws, outs=None, ws: torch.Tensor | None = None, stream=None):
     """Quantise a list of [rows, cols] CUDA tensors of one dtype (fp32 or bf16) with one
     sequence of launches. Returns the list of NF4Tensor."""
-    Ws = [W.view(1, -1) if W.dim() == 1 else W.contiguous() for W in Ws]
+    Ws = [W.view(1, -1) if W.dim() == 1 else _dense(stream, W)[0] for W in Ws]
     dt = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}[Ws[0].dtype]
     if any(W.dtype != Ws[0].dtype for W in Ws):
         raise ValueError("qlora_nf4_quantize_grouped: all tensors must share one dtype")
@@ -372,7 +381,7 @@ FMT4 = {"int4": 0, "fp4_e2m1": 1, "fp4_e3m0": 2}
 def qlora_fmt4_quantize(W: torch.Tensor, fmt: str, stream=None):
     """Blockwise Int4 / FP4 E2M1 / FP4 E3M0 (64-weight absmax blocks) of a fp32 or bf16 tensor.
     Returns (codes uint8 [ceil(n/2)], two codes per byte; absmax fp32 [ceil(n/64)])."""
-    W = W.contiguous()
+    W, = _dense(stream, W)
     n = W.numel()
     dt = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}[W.dtype]
     codes = torch.empty((n + 1) // 2, dtype=torch.uint8, device=W.device)
@@ -417,7 +426,7 @@ def qlora_fmt4_linear_fwd(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Te
     ydt = _DTYPES.get(Y.dtype)
     if ydt is None:
         raise ValueError("qlora_fmt4_linear_fwd: Y is bf16 or fp32")
-    Xc, cc, ac = X.contiguous(), codes.contiguous(), absmax.contiguous()
+    Xc, cc, ac = _dense(stream, X, codes, absmax)
     _launch("qlora_fmt4_linear_fwd", lib().qlora_fmt4_linear_fwd, dev, stream, Xc.data_ptr(), M, cc.data_ptr(),
             ac.data_ptr(), rows, cols, f, Y.data_ptr(), ydt)
     _hold(stream, Xc, cc, ac, Y)
@@ -514,9 +523,9 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     if Y is not None and (Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous()):
         raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
     dev = _same_device("qlora_moe_fwd", X, router, gate.codes, up.codes, down.codes, *(t for t in (Y, ws) if t is not None))
-    Xc, rc = X.contiguous(), router.contiguous()
+    Xc, rc = _dense(stream, X, router)
     if Y is None:
-        Y = torch.empty_like(Xc)
+        Y = torch.empty_strided((T, d), (d, 1), dtype=torch.bfloat16, device=X.device)
     # empty_strided is the cheapest of torch's allocations, a tenth of this call's host time
     experts = torch.empty_strided((T, k), (k, 1), dtype=torch.int32, device=X.device)
     weights = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=X.device)

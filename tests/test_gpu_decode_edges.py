@@ -48,3 +48,42 @@ def test_ends_of_the_range(fmt, M, rows, ec, ex):
             tol += 2.0 ** -8 * 1.001 * ref.abs() + 2.0 ** -134
         assert torch.isfinite(Y).all() and ((Y - ref).abs() <= tol).all()
     assert q.qlora_get_device_status() == q.QLORA_OK
+
+
+def strided(t):
+    """The same values in every second column of a wider tensor."""
+    wide = torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype, device=t.device)
+    wide[:, ::2] = t
+    return wide[:, ::2]
+
+
+def test_strided_inputs_on_another_stream():
+    # the copies that a call makes run where its kernels do, not behind what the current stream is busy with
+    g = torch.Generator(device="cuda").manual_seed(5)
+    M, rows, cols = 4, 320, 512
+    X = torch.randn(M, cols, generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn(rows, cols, generator=g, device="cuda") * 0.02
+    router = torch.randn(4, cols, generator=g, device="cuda")
+    codes, absmax = q.qlora_fmt4_quantize(W, "int4")
+    nf4 = q.qlora_nf4_quantize(W)
+    gate, up = (q.qlora_nf4_quantize(torch.randn(4 * 64, cols, generator=g, device="cuda")) for _ in range(2))
+    down = q.qlora_nf4_quantize(torch.randn(4 * cols, 64, generator=g, device="cuda"))
+    Xs, Ws, rs = strided(X), strided(W), strided(router)
+
+    def calls(X, W, router, stream):
+        out = [q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, "int4", stream=stream)]
+        out += q.qlora_moe_fwd(X, router, gate, up, down, 2, stream=stream)
+        out += q.qlora_fmt4_quantize(W, "int4", stream=stream)
+        for t in (q.qlora_nf4_quantize(W, stream=stream), *q.qlora_nf4_quantize_grouped([W], stream=stream)):
+            out += [t.codes, t.scale8, t.scale2, t.offset]
+        return out
+
+    want = calls(X, W, router, None)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    got = calls(Xs, Ws, rs, s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, [t.clone() for t in got]))
+    assert torch.equal(nf4.codes, got[-4])
