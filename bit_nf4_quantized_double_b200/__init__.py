@@ -211,6 +211,16 @@ class NF4Tensor:
     scale2: torch.Tensor   # float32 [ceil(nb/256)]
     offset: torch.Tensor   # float32 [1]
 
+    def __post_init__(self):
+        # the kernels go by rows and cols alone: a buffer that is shorter would be read or written past its end
+        _, ncode, nb, nb2 = nf4_sizes(self.rows, self.cols)
+        for name, dtype, n in (("codes", torch.uint8, ncode), ("scale8", torch.int8, nb), ("scale2", torch.float32, nb2),
+                               ("offset", torch.float32, 1)):
+            t = getattr(self, name)
+            if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.device != self.codes.device:
+                raise ValueError(f"NF4Tensor: {name} of a [{self.rows}, {self.cols}] tensor must be {n} contiguous {dtype} "
+                                 "values on the device of the codes")
+
     def ctype(self) -> _Tensor:
         return _Tensor(self.rows, self.cols, self.codes.data_ptr(), self.scale8.data_ptr(),
                        self.scale2.data_ptr(), self.offset.data_ptr())

@@ -28,3 +28,26 @@ def test_copies_are_made_on_the_calls_stream(monkeypatch):
     assert dense.is_contiguous() and torch.equal(dense, x) and made_on == ["s"]
     y = torch.zeros(3)
     assert q._dense("s", y)[0] is y
+
+
+def buffers(rows, cols):
+    t = q.nf4_empty(rows, cols, "cpu")
+    return dict(codes=t.codes, scale8=t.scale8, scale2=t.scale2, offset=t.offset)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 16421), (256, 128)])
+def test_stored_tensor_takes_its_buffers(rows, cols):
+    q.NF4Tensor(rows, cols, **buffers(rows, cols))
+    more = {k: torch.cat((t, t)) for k, t in buffers(rows, cols).items()}      # longer ones are fine
+    q.NF4Tensor(rows, cols, **more)
+
+
+@pytest.mark.parametrize("name", ["codes", "scale8", "scale2", "offset"])
+def test_stored_tensor_refuses_wrong_buffers(name):
+    # 256 x 1024: 131072 bytes of codes, 4096 and 16 constants
+    good = buffers(256, 1024)
+    t = good[name]
+    for bad in (t[:-1], t.to(torch.int32), torch.stack((t, t), 1)[:, 0][:max(t.numel(), 2)] if t.numel() > 1 else t[:0],
+                torch.empty_like(t, device="meta")):
+        with pytest.raises(ValueError, match=name if bad.device.type == "cpu" or name != "codes" else "scale8"):
+            q.NF4Tensor(256, 1024, **{**good, name: bad})
