@@ -528,8 +528,8 @@ def qlora_moe_fwd(X: torch.Tensor, router: torch.Tensor, gate: NF4Tensor, up: NF
     E, f = router.shape[0], down.cols
     if gate.cols != d:
         raise ValueError("qlora_moe_fwd: gate must have d columns")
-    if k < 0:
-        raise ValueError("qlora_moe_fwd: k must be positive")
+    if k < 0 or k > E:
+        raise ValueError("qlora_moe_fwd: k must be positive and at most the number of experts")
     if Y is not None and (Y.shape != (T, d) or Y.dtype != torch.bfloat16 or not Y.is_contiguous()):
         raise ValueError("qlora_moe_fwd: Y must be a contiguous bf16 [T, d] tensor")
     dev = _same_device("qlora_moe_fwd", X, router, gate.codes, up.codes, down.codes, *(t for t in (Y, ws) if t is not None))

@@ -51,3 +51,12 @@ def test_stored_tensor_refuses_wrong_buffers(name):
                 torch.empty_like(t, device="meta")):
         with pytest.raises(ValueError, match=name if bad.device.type == "cpu" or name != "codes" else "scale8"):
             q.NF4Tensor(256, 1024, **{**good, name: bad})
+
+
+def test_moe_refuses_more_experts_per_token_than_there_are():
+    # 2^32 + 2 would reach the C call as 2
+    x, router = torch.zeros(1, 128, dtype=torch.bfloat16), torch.zeros(4, 128)
+    t = [q.nf4_empty(r, c, "cpu") for r, c in ((256, 128), (256, 128), (512, 64))]
+    for k in (5, -1, 2 ** 32 + 2):
+        with pytest.raises(ValueError, match="k must be"):
+            q.qlora_moe_fwd(x, router, *t, k)
