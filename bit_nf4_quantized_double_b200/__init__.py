@@ -247,6 +247,8 @@ def nf4_empty(rows: int, cols: int, device="cuda") -> NF4Tensor:
 def _workspace(nbytes: int, device, ws=None):
     if nbytes == 0:
         return None, 0
+    if ws is not None and (not ws.is_contiguous() or ws.device != device):
+        raise ValueError("the workspace must be contiguous and on the device of the call's tensors")
     if ws is not None and ws.numel() * ws.element_size() >= nbytes:
         return ws, ws.numel() * ws.element_size()
     t = torch.empty(nbytes, dtype=torch.uint8, device=device)

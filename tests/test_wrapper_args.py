@@ -60,3 +60,13 @@ def test_moe_refuses_more_experts_per_token_than_there_are():
     for k in (5, -1, 2 ** 32 + 2):
         with pytest.raises(ValueError, match="k must be"):
             q.qlora_moe_fwd(x, router, *t, k)
+
+
+def test_workspace_with_strides_or_elsewhere_is_refused():
+    cpu = torch.device("cpu")
+    ws = torch.zeros(64, 2, dtype=torch.uint8)
+    assert q._workspace(100, cpu, ws)[0] is ws
+    with pytest.raises(ValueError, match="contiguous"):       # its 64 bytes would be taken from 64 in a row
+        q._workspace(64, cpu, ws[:, 0])
+    with pytest.raises(ValueError, match="device"):
+        q._workspace(64, torch.device("meta"), ws)
