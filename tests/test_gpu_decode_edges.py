@@ -87,3 +87,25 @@ def test_strided_inputs_on_another_stream():
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, [t.clone() for t in got]))
     assert torch.equal(nf4.codes, got[-4])
+
+
+# one CTA along the row, clusters of short rows (made while there are fewer tiles than SMs) and of long ones, tiles side by
+# side, the table and bit placement
+@pytest.mark.parametrize("fmt", ["int4", "fp4_e2m1", "fp4_e3m0"])
+@pytest.mark.parametrize("M,rows,cols", [(3, 1000, 256), (8, 300, 4096), (7, 640, 4160), (16, 500, 2048), (12, 600, 8192),
+                                         (4, 2600, 4096), (2, 5000, 2048), (2, 300, 33024)])
+def test_norm_of_the_error(fmt, M, rows, cols):
+    # per token, over the rows. mma cuts its 17 terms to 24 bits at the largest (about three times their rms): 2^-24 6 / 4 =
+    # 9e-8 of the norm; at most 4 + 15 + 7 additions after one another, each 2^-25 of a partial sum: 2^-25 sqrt(26 / 2) =
+    # 1.1e-7; token's power of two none, 1 / S and its product 2^-24 each: 8e-8. Together 1.7e-7, three times that allowed
+    S, mags = F.FORMATS[fmt]
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    X = torch.randn(M, cols, generator=g, device="cuda").to(torch.bfloat16)
+    codes = torch.randint(0, 256, (rows * cols // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    absmax = 0.05 * torch.exp(0.5 * torch.randn(rows * cols // 64, generator=g, device="cuda"))
+    c = torch.stack((codes >> 4, codes & 15), 1).reshape(-1).long()
+    table = torch.tensor(mags + [-m for m in mags], dtype=torch.float64, device="cuda")
+    y = X.double() @ (table[c].view(-1, 64) * (absmax.double() / S)[:, None]).view(rows, cols).t()
+    Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, fmt, out_dtype=torch.float32)
+    assert q.qlora_get_device_status() == q.QLORA_OK
+    assert ((Y.double() - y).norm(dim=1) <= 5e-7 * y.norm(dim=1)).all()
