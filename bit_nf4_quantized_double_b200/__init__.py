@@ -171,7 +171,10 @@ def _launch(what: str, fn, device: int, stream, *args):
 def _dense(stream, *tensors):
     """The tensors, those with strides as contiguous copies made on the call's stream: a caller can
     order `stream` behind whatever wrote the tensors, but not behind a copy queued elsewhere."""
-    if all(t.is_contiguous() for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return tensors
     with torch.cuda.stream(stream):                       # None: the current one
         return tuple(t.contiguous() for t in tensors)
