@@ -38,10 +38,12 @@
 // memory and a whole row per warp need no sums, but a warp per tile is 12 warps per SM at
 // [28672, 8192], too few to hide the latencies of the products.)
 //
-// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.4 / 32.1 us for E2M1 / E3M0 / Int4 (75 /
-// 64 / 63 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
-// weight, which is launch, first latencies and one sum. E2M1 with 8 tokens 28.3 us, with 9 to 16
-// tokens 43 to 44: two operand sets of 32 registers, twice the matrix instructions.
+// Measured, one token, [28672, 8192], 132 MB: 26.8 / 31.9 / 32.1 us for E2M1 / E3M0 / Int4 (75 /
+// 63 / 63 % of the measured copy rate; [114688, 8192], E2M1: 89 %); 4.4 us for the smallest
+// weight, which is launch, first latencies and one sum. E2M1 with 8 tokens 28.4 us, with 9 to 16
+// tokens 43 to 44: two operand sets of 32 registers at a limit of 128 (all but one of these forms
+// spill 12 to 112 bytes), twice the matrix instructions. Every 16 tokens read the codes again, one
+// group after the other: more tokens than a decode step has are not what this plan is for.
 #include <algorithm>
 
 #include "launch.h"
@@ -568,7 +570,7 @@ template <int FMT>
 cudaError_t f4_launch_tiles(F4Args &a, int64_t groups, cudaStream_t st) {
     if (a.M > 8) return f4_launch_form<FMT, 2, false>(a, groups, st);
     // The table pays for Int4 once every CTA has work: [28672, 8192] 32.1 us instead of 35.8, [4096, 4096] 5.5 instead of 5.8,
-    // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it). E3M0 takes 31.4 without one. Beside the sums of 16
+    // but [1001, 1984], half the CTAs, 4.54 instead of 4.47 (filling it). E3M0 takes 31.9 without one. Beside the sums of 16
     // tokens there is no room for it.
     if (FMT == QLORA_FMT4_INT4 && groups * a.nch >= num_sms() && shared_window_at(kF4Reserved))
         return f4_launch_form<FMT, 1, FMT == QLORA_FMT4_INT4>(a, groups, st);

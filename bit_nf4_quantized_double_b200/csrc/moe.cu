@@ -7,7 +7,7 @@
 // G, U [E F, D] and D [E D, F] hold the experts' rows one after the other.
 //
 // Two launches. k_moe_route: logits in fp64 (the products of bf16 values are exact there, and
-// neighbouring logits keep their order whatever the order of the sum), the tokens as scaled
+// logits keep their order down to fp64's rounding of a sum), the tokens as scaled
 // fp16, the grid barriers' counters cleared. k_moe_experts (cooperative, one CTA per SM): every
 // CTA chooses the experts (the same few hundred comparisons in each), then streams its share of
 // the gate and up tiles, a grid barrier, its share of the down tiles, a grid barrier, and its
@@ -24,10 +24,11 @@
 // constants into c = scale8 (scale2 / 127) + offset. With all of it in the sixteen warps a tile took
 // about 560 instructions of a warp, 200 of them the products. 24 warps leave 80 registers, 32 of
 // them tokens: what the roles share (shares of the phases, lists) stays in shared memory, since
-// every spill in the products costs (147 instead of 127 us for the second case below).
+// every spill in the products costs (147 instead of 127 us for the second case below); 52 bytes
+// are still spilled. The waits' votes (a warp gives up as one) take 0.5 to 1 %.
 //
-// Measured, (T, E, k, d, f): (1, 8, 2, 4096, 11008) 52 us, (4, ...) 120, (32, ...) 211, floors of
-// 21 / 58 / 85 at the measured copy rate; (1, 64, 8, 2048, 1024) 25 us, (16, ...) 69. About 16 us
+// Measured, (T, E, k, d, f): (1, 8, 2, 4096, 11008) 53 us, (4, ...) 121, (32, ...) 213, floors of
+// 21 / 58 / 85 at the measured copy rate; (1, 64, 8, 2048, 1024) 25 us, (16, ...) 70. About 16 us
 // are fixed: logits, choice (2.5 to 5.5), two grid barriers (1.2 each), first copies, last sums. A
 // group of 16 warps' tiles, 32 KB, takes 1.0 us (0.74 at the copy rate).
 //

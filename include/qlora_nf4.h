@@ -244,9 +244,10 @@ qlora_status qlora_linear_fwd_grouped(int64_t M, int count, const qlora_linear_d
  *            are NULL.
  *   ws       device workspace of qlora_moe_fwd_workspace() bytes (0 for shapes outside these
  *            rules). Calls that may run at the same time need a workspace each.
- * Logits are sums in fp64, so the choice does not depend on the order of a sum. The products
- * use the codebook and the activations as fp16 (2^-11 relative; activations scaled by powers of
- * two so that nothing overflows) and fp32 sums, the hidden values likewise; Y is rounded once.
+ * Logits are sums in fp64 in a fixed order: logits keep their order down to that rounding. The
+ * products use the codebook and the hidden values as fp16 (2^-11 relative), the activations as
+ * fp16 after scaling by a power of two (exact within 2^-31 of the largest of 256), and fp32
+ * sums, which block constants up to 2^100 keep in range; Y is rounded once.
  * Every output is a sum in a fixed order. A NaN logit counts as the largest; the outputs of a
  * token with a NaN or an infinity are what the formula gives for the experts chosen that way.
  * Two launches; the second is cooperative (one CTA per SM, two bounded grid barriers:
@@ -437,7 +438,7 @@ qlora_status qlora_fmt4_dequant(const uint8_t *codes, const float *absmax, int64
  * the weight's dequantisation before its rounding to bf16 (qlora_fmt4_dequant rounds each
  * weight; here products are exact, sums fp32, and Y is rounded once).
  *   X       bf16 [M, cols], 16-byte aligned; M >= 1 (made for M <= 16; more tokens read the
- *           codes again for every 16), M <= 1048560;
+ *           codes again for every 16, one group after the other), M <= 1048560;
  *   codes   the codes of a [rows, cols] weight as qlora_fmt4_quantize stores its
  *           rows * cols values, 16-byte aligned; cols % 64 == 0, any rows;
  *   absmax  fp32 [rows, cols / 64], 4-byte aligned;

@@ -80,7 +80,7 @@ def check(out, ref):
 
 
 # one block to several chunks of either width, odd block counts, tiles side by side, one token to more
-# than a job's sixteen per expert, one expert, all experts, many experts
+# than a job's eight per expert, one expert, all experts, many experts
 SHAPES = [(1, 64, 64, 1, 1), (2, 128, 192, 4, 2), (5, 256, 320, 7, 3), (1, 2048, 512, 32, 8), (7, 1088, 704, 13, 3),
           (20, 512, 256, 4, 4), (64, 320, 448, 16, 8), (17, 4096, 512, 2, 1), (4, 8192, 1024, 3, 2), (2, 4352, 4352, 3, 2),
           (40, 576, 128, 256, 16), (64, 64, 64, 64, 16), (33, 192, 576, 3, 1), (9, 128, 8256, 5, 2)]
