@@ -299,7 +299,7 @@ def qlora_nf4_dequant(q: NF4Tensor, out: torch.Tensor | None = None, stream=None
 def qlora_nf4_quantize_grouped(Ws, outs=None, ws: torch.Tensor | None = None, stream=None):
     """Quantise a list of [rows, cols] CUDA tensors of one dtype (fp32 or bf16) with one
     sequence of launches. Returns the list of NF4Tensor."""
-    Ws = [W.view(1, -1) if W.dim() == 1 else _dense(stream, W)[0] for W in Ws]
+    Ws = [_dense(stream, W.view(1, -1) if W.dim() == 1 else W)[0] for W in Ws]
     dt = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}[Ws[0].dtype]
     if any(W.dtype != Ws[0].dtype for W in Ws):
         raise ValueError("qlora_nf4_quantize_grouped: all tensors must share one dtype")

@@ -109,3 +109,10 @@ def test_norm_of_the_error(fmt, M, rows, cols):
     Y = q.qlora_fmt4_linear_fwd(X, codes, absmax, rows, fmt, out_dtype=torch.float32)
     assert q.qlora_get_device_status() == q.QLORA_OK
     assert ((Y.double() - y).norm(dim=1) <= 5e-7 * y.norm(dim=1)).all()
+
+
+def test_a_strided_vector_is_quantised_by_its_values():
+    W = torch.randn(2 * 16421, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    want = q.qlora_nf4_quantize(W[::2].clone())
+    for got in (q.qlora_nf4_quantize(W[::2]), *q.qlora_nf4_quantize_grouped([W[::2]])):
+        assert all(torch.equal(getattr(want, n), getattr(got, n)) for n in ("codes", "scale8", "scale2", "offset"))
