@@ -106,10 +106,10 @@ struct F4Args {
     uint32_t two2, two4, two8, two12;   // 2^2, 2^4, 2^8, 2^12
 };
 
-// A decoded operand times 2^scale is v(code) 2^j / S times `factor` below, with j such that the factor lies in [1, 2):
-// Int4 operands are m 2^-16 (m / 8 from the table), an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7). The power of
-// two goes into the tokens' 2^e, so that all sums hold Y / factor: neither do they overflow where Y does not, nor do they
-// lose more than a bit as subnormals where Y is none. (Applied at the end it made the sums 16 Y for E3M0.)
+// A decoded operand times 2^operand_scale times sum_factor is v(code) / S, the factor in [1, 2): Int4 operands are m 2^-16
+// (m / 8 from the table), an E3M0 code e is read as 2^(e - 3), its value is 2^(e - 7). The power of two goes into the
+// tokens' 2^e, so that all sums hold Y / factor: neither do they overflow where Y does not, nor do they lose more than a
+// bit as subnormals where Y is none. (All of it applied at the end made the sums 16 Y for E3M0.)
 __host__ __device__ constexpr int operand_scale(int fmt, bool table) {
     return fmt == QLORA_FMT4_INT4 ? (table ? 0 : 13) : fmt == QLORA_FMT4_FP4_E2M1 ? -3 : -4;
 }
